@@ -172,6 +172,58 @@ SVLA_API svla_status svla_train_step(svla_handle* h, const void* kv_cache, const
 /* Number of float32 gradient elements of svla_train_step (0 without a training workspace). */
 SVLA_API size_t svla_train_grad_elems(const svla_handle* h);
 
+/* Tensors and settings of an AdamW step (svla_train_update, svla_op_adamw;
+ * the formulas stand at svla_op_adamw). */
+typedef struct svla_adamw_tensor {
+  void* param;          /* param_type [n], updated                     */
+  const void* grad;     /* grad_type [n]                               */
+  void* m;              /* float32 [n] or uint8 codes [n], updated     */
+  void* v;
+  float* m_scale;       /* 8-bit states: [ceil(n / 256)], updated      */
+  float* v_scale;
+  void* copy;           /* NULL, or bf16 [n]: the updated param        */
+  int64_t n;
+  int decay;            /* nonzero: weight_decay applies               */
+} svla_adamw_tensor;
+
+typedef struct svla_adamw_args {
+  int param_type, grad_type;   /* SVLA_TYPE_F32 or SVLA_TYPE_BF16      */
+  int state_bits;              /* 32 or 8                              */
+  double lr, beta1, beta2, eps, weight_decay;
+  double max_norm;             /* 0: no clip                           */
+  int64_t step;                /* counts from 1                        */
+  uint64_t seed;               /* 8-bit states: key of the rounding    */
+  const int64_t* step_device;
+  const double* lr_device;
+} svla_adamw_args;
+
+/* The update that follows svla_train_step: one AdamW step on the expert's and
+ * the heads' tensors, whose bf16 rounding becomes the weights that the next
+ * svla_train_step of this handle reads ("noeira docs, SmolVLA" §Fine-tuning).
+ *   master: device float32, svla_train_grad_elems(h) elements in the order of
+ *     svla_train_step's gradients: the weights, updated in place (start them
+ *     from the blob's, or from svla_train_weights).
+ *   grads: device float32, as svla_train_step wrote them.
+ *   m, v: the moments, float32 or 8-bit codes [svla_train_grad_elems(h)];
+ *   m_scale, v_scale: 8-bit moments only, float32 [svla_train_scale_elems(h)].
+ *   args: param_type and grad_type SVLA_TYPE_F32; weight_decay applies to the
+ *     matrices, not to gains and biases. The tensor index is the tensor's place
+ *     among the gradients (0 for the first expert layer's in_norm).
+ *   grad_norm: with a clip, device float32 scalar or NULL.
+ * 16-byte aligned buffers (8 for 8-bit codes) take wide accesses. The weights of
+ * svla_prefill, svla_denoise and svla_sample stay those given at creation: a
+ * handle for them is created from the updated weights. Stream-ordered; needs a
+ * handle created with SVLA_CREATE_TRAIN (else SVLA_ERR_UNSUPPORTED). */
+SVLA_API svla_status svla_train_update(svla_handle* h, float* master, const float* grads, void* m, void* v,
+                                       float* m_scale, float* v_scale, const svla_adamw_args* args,
+                                       float* grad_norm, void* stream);
+/* Number of float32 scales of each 8-bit moment (one for 256 elements of a
+ * tensor, every tensor starting anew; 0 without a training workspace). */
+SVLA_API size_t svla_train_scale_elems(const svla_handle* h);
+/* Copy the weights that the next svla_train_step reads to `out` (device bf16,
+ * svla_train_grad_elems(h) elements, the blob's order). */
+SVLA_API svla_status svla_train_weights(svla_handle* h, void* out, void* stream);
+
 /* Free everything the handle owns (synchronises its device first). NULL is ok. */
 SVLA_API svla_status svla_destroy(svla_handle* h);
 
@@ -306,6 +358,10 @@ SVLA_API const char* svla_status_string(svla_status s);
  * path so each can be checked on its own; they use the same code as the path.
  * ------------------------------------------------------------------------- */
 
+/* Element types of the arguments that say so. */
+#define SVLA_TYPE_F32       0
+#define SVLA_TYPE_BF16      1
+
 /* Epilogues of svla_op_gemm. */
 #define SVLA_EPI_F32        0   /* C(f32)  = acc (+ bias)                     */
 #define SVLA_EPI_BF16       1   /* C(bf16) = acc (+ bias)                     */
@@ -374,6 +430,83 @@ SVLA_API int svla_op_gemm_w8_tile_n(int M, int N, int K);
 /* RMSNorm (reading 8): y(bf16)[M, D] = x(f32)[M, D] / sqrt(mean(x^2) + eps) * g(bf16)[D]. */
 SVLA_API svla_status svla_op_rmsnorm(const float* x, const void* g, int M, int D, float eps,
                             void* y, void* stream);
+
+/* LayerNorm, the norm of the vision side's layers (SigLIP, upstream of
+ * svla_assemble_prefix: "noeira docs, SmolVLA" §Architecture), beside
+ * svla_op_rmsnorm, with the backward pass that training them needs.
+ *   forward, per row of D:  mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps),
+ *     y = (x - mu) r gamma + beta
+ *   backward, xh = (x - mu) r, w = dy gamma:
+ *     dx = r (w - mean(w) - xh mean(w xh)), dgamma = sum dy xh, dbeta = sum dy
+ * Statistics and sums are fp32; y and dx are rounded once, to nearest even.
+ *   x, dy, y, dx: device, SVLA_TYPE_F32 or SVLA_TYPE_BF16 each (dy has y's
+ *     type, dx has x's), row strides in elements, >= D, of any alignment.
+ *   gamma, beta: device, w_type [D]; beta NULL: 0.
+ *   mean, rstd: device float32 [M], written by the forward (each may be NULL
+ *     there) and read by the backward.
+ *   dgamma, dbeta: device float32 [D], written in full (not added to), each
+ *     NULL to leave out. Their sums run in an order that M and D fix: results
+ *     are bitwise reproducible.
+ *   y may be x itself and dx may be x or dy itself (same pointer, type and
+ *     stride); any other overlap of an output with another argument is
+ *     SVLA_ERR_ARG.
+ *   M >= 0 (M = 0 writes no rows and zero gradients), 1 <= D <= 16384, eps > 0.
+ *   workspace: device, 4-byte aligned, at least
+ *     svla_op_layernorm_backward_workspace_bytes(M, D) bytes (0 for few rows,
+ *     or without dgamma and dbeta: then it may be NULL); nothing is kept in it
+ *     between calls. Calls that may overlap on the GPU, replayed graphs among
+ *     them, need workspaces of their own. */
+SVLA_API svla_status svla_op_layernorm(const void* x, int x_type, int ldx, const void* gamma, const void* beta,
+                                       int w_type, int M, int D, float eps, void* y, int y_type, int ldy,
+                                       float* mean, float* rstd, void* stream);
+SVLA_API svla_status svla_op_layernorm_backward(const void* dy, int y_type, int lddy, const void* x, int x_type,
+                                                int ldx, const void* gamma, int w_type, const float* mean,
+                                                const float* rstd, int M, int D, void* dx, int lddx, float* dgamma,
+                                                float* dbeta, void* workspace, size_t workspace_bytes, void* stream);
+SVLA_API size_t svla_op_layernorm_backward_workspace_bytes(int M, int D);
+
+/* One AdamW step over many tensors, in place: the update that follows
+ * svla_train_step ("noeira docs, SmolVLA" §Fine-tuning), for any list of
+ * tensors (svla_train_update takes the expert's). Per element, each product
+ * and sum rounded to fp32, t the step number:
+ *   g' = c g,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   p  = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * (weight_decay only where the tensor's `decay` is set), then copy = bf16(p).
+ * Clip, with max_norm > 0: c = min(1, max_norm / (G + 1e-6)), G the square root
+ * of the sum of g^2 over ALL tensors (fp64), written to grad_norm. If G is not
+ * finite the step is skipped: nothing but grad_norm is written. max_norm =
+ * INFINITY measures G and skips, without clipping. With max_norm = 0 c is 1,
+ * grad_norm is not written, and a gradient that is not finite makes its
+ * element's parameter and moments NaN.
+ * state_bits 32: m and v are float32 [n].
+ * state_bits 8: m holds e4m3 codes and v e5m2 codes (uint8 [n]), m_scale and
+ *   v_scale a float32 for every 256 consecutive elements of the tensor
+ *   (ceil(n / 256)): moment = code * scale. The scale is the power of two that
+ *   puts the largest magnitude of its 256 into [2^7, 2^8) (m) or [2^14, 2^15)
+ *   (v); 0 where all are 0. Magnitudes are rounded up with the probability of
+ *   their distance to the lower code, from 16 random bits: Philox4x32-10 with
+ *   key = seed, counter {k / 8 low, k / 8 high, t, tensor index} for element k,
+ *   half k % 8 of the 128 bits (low half of a word first). No subnormal codes:
+ *   an m then below 2^-6 of its scale becomes 0, a v > 0 is at least 2^-14 of it.
+ *   Zero bytes are a valid start (all moments 0).
+ * The device pointers and n of all tensors; the table is read during the call
+ * only. n = 0 is skipped. Pointers need their element type's alignment;
+ * tensors whose pointers are all 16-byte aligned (8 for 8-bit codes) are read
+ * in wide accesses. Memory that is written may not overlap any other range of
+ * the call (SVLA_ERR_ARG), so no tensor may be listed twice; gradients may be
+ * shared.
+ *   step_device, lr_device: NULL, or a device int64 / double read when the step
+ *     runs instead of `step` / `lr`: a captured and replayed call then takes
+ *     each replay's values (the host's are fixed at capture).
+ *   workspace: device, 8-byte aligned, svla_op_adamw_workspace_bytes(n_tensors)
+ *     bytes, with a clip only (else NULL); nothing is kept in it between calls.
+ *     Calls that may overlap on the GPU, replayed graphs among them, need
+ *     workspaces of their own.
+ * The result does not depend on the tensors' alignment or on the other tensors
+ * but through G and the tensor index; it is bitwise reproducible. */
+SVLA_API svla_status svla_op_adamw(const svla_adamw_tensor* tensors, int n_tensors, const svla_adamw_args* args,
+                                   void* workspace, size_t workspace_bytes, float* grad_norm, void* stream);
+SVLA_API size_t svla_op_adamw_workspace_bytes(int n_tensors);
 
 /* svla_op_gemm without a workspace argument, for callers that cannot allocate
  * GPU memory themselves: code that must not call cudaMalloc once it is running

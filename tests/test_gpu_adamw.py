@@ -1,0 +1,472 @@
+"""svla_op_adamw and svla_train_update on the GPU against the oracle.
+
+What is compared how:
+  * moments in 32 bits, codes and scales in 8: bit for bit against the oracle in
+    float32 (every product and sum is one IEEE operation on both sides);
+  * parameters: against the oracle in float64 started from those same values,
+    with every rounding counted in units of 2^-24. m' may cancel, so its error
+    is relative to A = |b1 m| + |c1 g'|: the clip factor, g c, a coefficient and
+    a product for each summand and the sum make at most 5 A. denom: g'^2 has
+    twice (clip factor, product), square, coefficient and product, v the sum: 8,
+    of which the root halves to 4; the root, 1 / sqrt(1 - b2^t), its product
+    and the sum with eps: 8 in all. Quotient, step size and product: 3.
+    Together 16 units of A lr / (1 - b1^t) / denom. p (1 - lr wd) has the
+    factor, the product, and p' the last rounding: 2 |p| + |p'| (4 of each
+    allowed). bf16 parameters and copies add half a bf16 step: 2^-8 |p'|.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import synth  # noqa: E402
+from oracle import optim as oo  # noqa: E402
+from vision_language_action_b200 import _abi  # noqa: E402
+from vision_language_action_b200.runtime import AdamW, SmolVLA  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+DEV = "cuda:0"
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+U = 2.0 ** -24
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def make(sizes, p="f32", g="f32", bits=32, seed=0, offset=0, fresh=False, spread=1.0):
+    """Tensors of the sizes as parts of flat buffers that begin `offset` elements in."""
+    gen = torch.Generator().manual_seed(seed)
+    n = sum(sizes)
+
+    def flat(x, dt):
+        buf = torch.empty(n + offset, dtype=dt, device=DEV)
+        buf[offset:] = x.to(dt).to(DEV)
+        return list(buf[offset:].split(list(sizes)))
+
+    rnd = lambda s: torch.randn(n, generator=gen) * s
+    st = dict(p=flat(rnd(0.05), DT[p]), g=flat(rnd(1e-3) * torch.exp(spread * rnd(1.0)), DT[g]))
+    if bits == 32:
+        st["m"] = flat(rnd(0.0 if fresh else 3e-4), torch.float32)
+        st["v"] = flat(rnd(0.0 if fresh else 1e-3) ** 2, torch.float32)
+        st["ms"] = st["vs"] = None
+    else:
+        # any code but NaN and infinity is a legal start, subnormal ones too
+        codes = torch.randint(0, 256, (n,), generator=gen, dtype=torch.int64)
+        m = torch.where((codes & 0x7F) == 0x7F, 0, codes)
+        v = torch.randint(0, 0x7C, (n,), generator=gen, dtype=torch.int64)
+        per = [(k + 255) // 256 for k in sizes]
+        exps = torch.randint(-24, -14, (sum(per),), generator=gen).float()
+        st["m"] = flat((m * (not fresh)).to(torch.uint8).view(torch.float8_e4m3fn), torch.float8_e4m3fn)
+        st["v"] = flat((v * (not fresh)).to(torch.uint8).view(torch.float8_e5m2), torch.float8_e5m2)
+        st["ms"] = list((2.0 ** exps).to(DEV).split(per))
+        st["vs"] = list((2.0 ** (2 * exps + 8)).to(DEV).split(per))
+    return st
+
+
+def codes_of(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def start_moments(st, bits):
+    if bits == 32:
+        return [x.cpu().numpy() for x in st["m"]], [x.cpu().numpy() for x in st["v"]]
+    out = []
+    for c, s, fmt in ((st["m"], st["ms"], oo.E4M3), (st["v"], st["vs"], oo.E5M2)):
+        out.append([(oo.decode(codes_of(x), fmt) * np.repeat(s_.cpu().numpy().astype(np.float64), 256)[:x.numel()])
+                    .astype(np.float32) for x, s_ in zip(c, s)])
+    return out
+
+
+def check_step(st, before, bits, hp, step, decay, seed, max_norm, copies=None, tensor0=0):
+    """`before`: (p, g, m, v) numpy lists from before the step."""
+    P, G, M, V = before
+    norm = oo.grad_norm(G)
+    c = float(np.float32(oo.clip_factor(norm, max_norm)))
+    for i, (p, g, m, v) in enumerate(zip(P, G, M, V)):
+        if p.size == 0:
+            continue
+        _, m1, v1 = oo.adamw(p, g, m, v, *hp, step, decay[i], c, dtype=np.float32)
+        if bits == 32:
+            assert np.array_equal(st["m"][i].cpu().numpy(), m1), i
+            assert np.array_equal(st["v"][i].cpu().numpy(), v1), i
+        else:
+            u = oo.random16(p.size, tensor0 + i, step, seed)
+            for got, scale, x, fmt, keep in ((st["m"][i], st["ms"][i], m1, oo.E4M3, False),
+                                             (st["v"][i], st["vs"][i], v1, oo.E5M2, True)):
+                codes, s = oo.encode(x, u, fmt, keep)
+                assert np.array_equal(scale.cpu().numpy(), s), i
+                assert np.array_equal(codes_of(got), codes), i
+        p1, _, _ = oo.adamw(p, g, m, v, *hp, step, decay[i], oo.clip_factor(norm, max_norm))
+        lr, b1, b2, eps = hp[:4]
+        gc = np.asarray(g, np.float64) * c
+        v64 = b2 * v.astype(np.float64) + (1 - b2) * gc * gc
+        moved = (b1 * np.abs(m.astype(np.float64)) + (1 - b1) * np.abs(gc)) * lr / (1 - b1 ** float(step)) / (
+            np.sqrt(v64 / (1 - b2 ** float(step))) + eps)
+        tol = U * 4 * (np.abs(p) + np.abs(p1)) + 16 * U * moved + 1e-45
+        got = np64(st["p"][i])
+        if st["p"][i].dtype == torch.bfloat16:
+            tol = tol + 2.0 ** -8 * np.abs(p1)
+        assert (np.abs(got - p1) <= tol).all(), (i, np.max(np.abs(got - p1) / tol))
+        if copies is not None and copies[i] is not None:
+            assert torch.equal(copies[i], st["p"][i].to(torch.bfloat16)), i
+    return norm
+
+
+def run_case(sizes, p="f32", g="f32", bits=32, max_norm=0.0, step=1, seed=11, offset=0, fresh=False, copy=True,
+             hp=(1e-3, 0.9, 0.999, 1e-8, 0.1), spread=1.0, steps=1):
+    st = make(sizes, p, g, bits, seed, offset, fresh, spread)
+    n = len(sizes)
+    decay = [(i * 7 + 1) % 3 != 0 for i in range(n)]
+    copies = [torch.zeros(k, dtype=torch.bfloat16, device=DEV) if i % 4 != 3 else None for i, k in enumerate(sizes)] \
+        if copy else None
+    opt = AdamW(st["p"], lr=hp[0], betas=hp[1:3], eps=hp[3], weight_decay=hp[4], state_bits=bits, max_norm=max_norm,
+                copies=copies, decay=decay, seed=(seed << 33) + 5, step=step - 1,
+                state=(st["m"], st["v"], st["ms"], st["vs"]))
+    for k in range(steps):
+        M, V = start_moments(st, bits)
+        before = ([x.float().cpu().numpy() for x in st["p"]], [x.float().cpu().numpy() for x in st["g"]], M, V)
+        opt.step(st["g"])
+        norm = check_step(st, before, bits, hp, step + k, decay, (seed << 33) + 5, max_norm, copies)
+        if max_norm:
+            assert abs(float(opt.grad_norm) - norm) <= U * norm
+    return st, opt
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("p,g", [("f32", "f32"), ("f32", "bf16"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("offset", [0, 1, 4])
+def test_types_and_alignments(p, g, bits, offset):
+    run_case([256, 1, 255, 257, 4096, 8, 2048 + 13, 31], p, g, bits, step=3, offset=offset, seed=offset + 1)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("sizes", [[1], [7], [256], [255], [257], [0, 5, 0], [0, 0, 300, 0], [100_003], [1 << 20]])
+def test_sizes(sizes, bits):
+    run_case(sizes, bits=bits, step=2, max_norm=0.5)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("count", [399, 400, 401, 1203])
+def test_many_tensors(count, bits):
+    """More tensors than one launch's table holds, empty ones among them; the norm goes over all of them."""
+    rng = np.random.default_rng(count)
+    sizes = [int(x) for x in rng.integers(0, 600, count)]
+    run_case(sizes, bits=bits, max_norm=0.3, step=5, spread=0.5)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("max_norm", [1e-6, 0.2, 1e6, float("inf")])
+def test_clip(max_norm, bits):
+    run_case([5000, 3, 777, 64 * 256], bits=bits, max_norm=max_norm, step=2)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("p", ["f32", "bf16"])
+def test_from_zero_over_several_steps(p, bits):
+    run_case([1000, 33, 512], p=p, bits=bits, fresh=True, steps=6, max_norm=1.0)
+
+
+@pytest.mark.parametrize("step", [1, 2, 1000, 10 ** 6, 2 ** 31 + 3, 2 ** 33 + 1])
+def test_step_numbers(step):
+    run_case([300, 9], bits=8, step=step)
+
+
+@pytest.mark.parametrize("hp", [(0.0, 0.9, 0.999, 1e-8, 0.1), (1e-2, 0.0, 0.0, 1e-3, 0.0), (1e-3, 0.5, 0.9999, 1e-15, 10.0),
+                                (3.0, 0.9, 0.95, 1.0, 0.0)])
+def test_settings(hp):
+    for bits in (32, 8):
+        run_case([700, 3], bits=bits, step=4, hp=hp, spread=0.3)
+
+
+def test_wide_gradient_range_in_8_bits():
+    """Magnitudes from far below float32's normal range to far above one: zero, tiny, huge in one block and apart."""
+    st, _ = run_case([512, 256, 256], bits=8, spread=0.1, step=3)
+    for scale in (1e-30, 1e-24, 1e12):
+        st = make([512, 300], bits=8, fresh=True, seed=4)
+        for g in st["g"]:
+            g.mul_(scale)
+            g[::7] = 0
+        st["g"][1].zero_()
+        opt = AdamW(st["p"], state_bits=8, seed=9, state=(st["m"], st["v"], st["ms"], st["vs"]))
+        M, V = start_moments(st, 8)
+        before = ([x.cpu().numpy() for x in st["p"]], [x.cpu().numpy() for x in st["g"]], M, V)
+        opt.step(st["g"])
+        with np.errstate(all="ignore"):
+            check_step(st, before, 8, (1e-3, 0.9, 0.999, 1e-8, 1e-2), 1, [True, True], 9, 0.0)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_gradients_that_are_not_finite(bad, bits):
+    """Without a clip only the element concerned is lost; with one the whole step is skipped."""
+    sizes = [600, 300]
+    ref = make(sizes, bits=bits, seed=6)
+    opt = AdamW(ref["p"], state_bits=bits, seed=1, state=(ref["m"], ref["v"], ref["ms"], ref["vs"]))
+    opt.step(ref["g"])
+    st = make(sizes, bits=bits, seed=6)
+    st["g"][0][300] = bad
+    AdamW(st["p"], state_bits=bits, seed=1, state=(st["m"], st["v"], st["ms"], st["vs"])).step(st["g"])
+    for i in range(2):
+        keep = torch.ones(sizes[i], dtype=torch.bool, device=DEV)
+        if i == 0:
+            keep[300] = False
+            assert torch.isnan(st["p"][0][300])
+            if bits == 8:
+                assert int(st["m"][0].view(torch.uint8)[300]) == 0x7F and int(st["v"][0].view(torch.uint8)[300]) == 0x7F
+                keep[256:512] = False  # its block's scale may lose its largest element
+        assert torch.equal(st["p"][i][keep], ref["p"][i][keep]) or bits == 8
+        assert torch.equal(st["m"][i].view(torch.uint8).view(sizes[i], -1)[keep],
+                           ref["m"][i].view(torch.uint8).view(sizes[i], -1)[keep])
+    skip, untouched = make(sizes, bits=bits, seed=6), make(sizes, bits=bits, seed=6)
+    skip["g"][0][300] = bad
+    copies = [torch.full((k,), 7.0, dtype=torch.bfloat16, device=DEV) for k in sizes]
+    opt = AdamW(skip["p"], state_bits=bits, max_norm=1.0, copies=copies, state=(skip["m"], skip["v"], skip["ms"], skip["vs"]))
+    opt.step(skip["g"])
+    assert not torch.isfinite(opt.grad_norm).item()
+    for k in ("p", "m", "v", "ms", "vs"):
+        for a, b in zip(skip[k] or [], untouched[k] or []):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert all((c == 7).all() for c in copies)
+
+
+def test_nothing_beside_the_tensors_is_written():
+    """Neighbours in the same buffers keep their bytes, in front and behind."""
+    for bits in (32, 8):
+        for lo, n in ((0, 250), (8, 256), (3, 513), (16, 2048), (1, 1)):
+            total = lo + n + 40
+            p, m32 = torch.full((total,), 3.0, device=DEV), torch.zeros(total, device=DEV)
+            codes = torch.zeros(total, dtype=torch.uint8, device=DEV)
+            g = torch.ones(total, device=DEV)
+            per = (n + 255) // 256
+            scales = torch.full((per + 2,), 5.0, device=DEV)
+            scales2, copy = scales.clone(), torch.full((total,), 9.0, dtype=torch.bfloat16, device=DEV)
+            cut = slice(lo, lo + n)
+            if bits == 32:
+                v32 = m32.clone()
+                state = ([m32[cut]], [v32[cut]], None, None)
+            else:
+                vc = codes.clone()
+                state = ([codes[cut].view(torch.float8_e4m3fn)], [vc[cut].view(torch.float8_e5m2)],
+                         [scales[1:1 + per]], [scales2[1:1 + per]])
+            AdamW([p[cut]], state_bits=bits, copies=[copy[cut]], state=state).step([g[cut]])
+            outside = torch.ones(total, dtype=torch.bool, device=DEV)
+            outside[cut] = False
+            assert (p[outside] == 3).all() and (copy[outside] == 9).all() and (p[cut] != 3).all()
+            if bits == 32:
+                assert (m32[outside] == 0).all() and (v32[outside] == 0).all() and (m32[cut] > 0).all()
+            else:
+                assert (codes[outside] == 0).all() and (vc[outside] == 0).all() and (codes[cut] > 0).all()
+                assert scales[0] == scales[-1] == 5 and scales2[0] == scales2[-1] == 5
+
+
+def test_results_do_not_depend_on_alignment_or_company():
+    """The same tensor alone and aligned, in a list, and at an odd address: the same bits."""
+    for bits in (32, 8):
+        outs = []
+        for offset in (0, 3):
+            st = make([5000], bits=bits, seed=2, offset=offset)
+            opt = AdamW(st["p"], state_bits=bits, seed=4, state=(st["m"], st["v"], st["ms"], st["vs"]))
+            for _ in range(3):
+                opt.step(st["g"])
+            outs.append(st)
+        for k in ("p", "m", "v"):
+            assert torch.equal(outs[0][k][0].view(torch.uint8), outs[1][k][0].view(torch.uint8)), (bits, k)
+
+
+def test_owned_state_and_shared_gradients():
+    """Moments that the optimiser allocates itself start at zero; one gradient may serve two parameters."""
+    g = torch.randn(1000, device=DEV) * 1e-3
+    for bits in (32, 8):
+        ps = [torch.ones(1000, device=DEV), torch.ones(1000, device=DEV)]
+        opt = AdamW(ps, lr=1e-2, weight_decay=0.0, state_bits=bits)
+        opt.step([g, g])
+        assert torch.equal(ps[0], ps[1])
+        # from zero moments the first step is lr g / (|g| + eps) whatever the betas
+        g64 = g.double()
+        assert (ps[0].double() - (1 - 1e-2 * g64 / (g64.abs() + 1e-8))).abs().max() <= 4 * U + 16 * U * 1e-2
+
+
+def test_stream_and_repeatability():
+    a, b = make([70_000, 11], bits=8, seed=3), make([70_000, 11], bits=8, seed=3)
+    side = torch.cuda.Stream()
+    for st, stream in ((a, None), (b, side)):
+        opt = AdamW(st["p"], state_bits=8, max_norm=0.1, state=(st["m"], st["v"], st["ms"], st["vs"]))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            opt.step(st["g"], stream=stream)
+        torch.cuda.synchronize()
+    for k in ("p", "m", "v"):
+        for x, y in zip(a[k], b[k]):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_captured_steps_count_on(bits):
+    """A captured step, replayed: the device counter and the device learning rate make each replay the next step."""
+    lr = torch.full((1,), 1e-3, dtype=torch.float64, device=DEV)
+    a, b = make([3000, 500], bits=bits, seed=8), make([3000, 500], bits=bits, seed=8)
+    kw = dict(state_bits=bits, max_norm=0.5, seed=3)
+    eager = AdamW(a["p"], state=(a["m"], a["v"], a["ms"], a["vs"]), **kw)
+    graphed = AdamW(b["p"], lr=lr, capturable=True, state=(b["m"], b["v"], b["ms"], b["vs"]), **kw)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        graphed.step(b["g"])
+    for k in range(4):
+        rate = 1e-3 * (k + 1)
+        lr.fill_(rate)
+        graph.replay()
+        eager.step(a["g"], lr=rate)
+    torch.cuda.synchronize()
+    assert int(graphed.step_tensor) == 4
+    for k in ("m", "v"):
+        for x, y in zip(a[k], b[k]):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    for x, y in zip(a["p"], b["p"]):
+        # the device's pow may round the last bit of 1 - beta^t apart from the host's: 2 steps of the update
+        assert torch.allclose(x, y, rtol=2 ** -22, atol=1e-3 * 2 ** -20)
+
+
+def test_python_refusals():
+    p = [torch.zeros(10, device=DEV), torch.zeros(6, device=DEV)]
+    g = [torch.zeros(10, device=DEV), torch.zeros(6, device=DEV)]
+    with pytest.raises(ValueError):
+        AdamW([p[0], p[1].to(torch.bfloat16)])
+    with pytest.raises(ValueError):
+        AdamW([torch.zeros(4, 6, device=DEV).t()])
+    with pytest.raises(ValueError):
+        AdamW(p, state_bits=16)
+    with pytest.raises(ValueError):
+        AdamW(p, decay=[True])
+    with pytest.raises(ValueError):
+        AdamW(p, copies=[torch.zeros(10, device=DEV), None])
+    with pytest.raises(ValueError):
+        AdamW(p, state=([torch.zeros(10, device=DEV)] * 2, g, None, None))
+    with pytest.raises(ValueError):
+        AdamW(p, lr=torch.zeros(1, device=DEV))
+    opt = AdamW(p)
+    for bad in ([g[0]], [g[0], g[0]], [g[0], g[1].to(torch.bfloat16)], [g[0], g[1].cpu()], [g[0].half(), g[1].half()]):
+        with pytest.raises(ValueError):
+            opt.step(bad)
+    with pytest.raises(_abi.SvlaError):
+        AdamW([p[0], p[0]]).step([g[0], g[0]])
+    assert opt.steps == 0
+
+
+# ----------------------------------------------------------------------
+# the expert's fine-tune: train_step -> train_update -> train_step
+# ----------------------------------------------------------------------
+def tiny_case(B=2, L=24, Hc=8, seed=7):
+    s = synth.SHAPES["tiny"]
+    wb = synth.gen_weights(s, seed, random_affine=True)
+    rng = np.random.default_rng(seed)
+    kv = torch.from_numpy(rng.standard_normal((2, s.p_layers, B, L, s.p_kv_width)).astype(np.float32)).to(DEV)
+    valid = torch.ones(B, L, dtype=torch.uint8, device=DEV)
+    f = lambda *shape: torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(DEV)
+    return s, wb, (kv.to(torch.bfloat16), valid, f(B, Hc, s.action_dim), f(B, Hc, s.action_dim),
+                   torch.tensor([0.3, 0.8], device=DEV)[:B])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_train_update_runs_with_the_training_step(bits):
+    s, wb, batch = tiny_case()
+    m = SmolVLA(s, synth.pack_blob(s, wb), max_batch=2, max_prefix=24, max_chunk=8, train=True)
+    other = None
+    try:
+        names = [(k, shp) for k, shp in synth.manifest(s) if not k.startswith("p")]
+        sizes = [int(np.prod(shp)) for _, shp in names]
+        decay = [len(shp) == 2 for _, shp in names]
+        assert sum(sizes) == m.train_weights().numel()
+        start = np.concatenate([wb[k].ravel() for k, _ in names])
+        assert np.array_equal(m.train_weights().view(torch.int16).cpu().numpy().view(np.uint16), start)
+        master = m.train_weights().float()
+        mom = m.new_moments(bits)
+        norm = torch.zeros(1, device=DEV)
+        hp = dict(lr=5e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, max_norm=0.05, seed=77)
+        # the same steps through the list of tensors
+        ref = master.clone()
+        copy = torch.zeros_like(ref, dtype=torch.bfloat16)
+        per = [(n + 255) // 256 for n in sizes]
+        mom2 = [None if x is None else x.clone() for x in mom]
+        parts = lambda x, k: None if x is None else list(x.split(k))
+        opt = AdamW(parts(ref, sizes), lr=5e-3, betas=(0.9, 0.95), weight_decay=0.1, max_norm=0.05, seed=77,
+                    state_bits=bits, decay=decay, copies=parts(copy, sizes),
+                    state=(parts(mom2[0], sizes), parts(mom2[1], sizes), parts(mom2[2], per), parts(mom2[3], per)))
+        for step in range(1, 4):
+            loss, grads = m.train_step(*batch)
+            m.train_update(master, grads, mom, step, grad_norm=norm, **hp)
+            opt.step(list(grads.split(sizes)))
+            assert torch.equal(master, ref) and torch.equal(m.train_weights(), copy)
+            assert torch.equal(norm, opt.grad_norm) and float(norm) > 0.05
+            for x, y in zip(mom, mom2):
+                assert x is None or torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+        # the next training step is that of a handle created from the updated weights, biases included
+        loss, grads = m.train_step(*batch)
+        new, at = dict(wb), 0
+        bitsw = m.train_weights().view(torch.int16).cpu().numpy().view(np.uint16)
+        for (k, shp), n in zip(names, sizes):
+            new[k] = bitsw[at:at + n].reshape(shp).copy()
+            at += n
+        assert all(not np.array_equal(new[k], wb[k]) for k, _ in names)
+        other = SmolVLA(s, synth.pack_blob(s, new), max_batch=2, max_prefix=24, max_chunk=8, train=True)
+        loss2, grads2 = other.train_step(*batch)
+        assert torch.equal(loss, loss2) and torch.equal(grads, grads2)
+        # what the handle answers with is unchanged
+        noise = batch[3]
+        a, _ = m.denoise(batch[0], batch[1], noise, 2)
+        fresh = SmolVLA(s, synth.pack_blob(s, wb), max_batch=2, max_prefix=24, max_chunk=8)
+        b, _ = fresh.denoise(batch[0], batch[1], noise, 2)
+        assert torch.equal(a, b)
+        fresh.close()
+        # a gradient that is not finite skips the step
+        before = master.clone()
+        grads[5] = float("nan")
+        m.train_update(master, grads, mom, 4, grad_norm=norm, **hp)
+        assert torch.equal(master, before) and torch.isnan(norm).item()
+    finally:
+        m.close()
+        if other is not None:
+            other.close()
+
+
+def test_train_update_refusals():
+    s, wb, batch = tiny_case()
+    plain = SmolVLA(s, synth.pack_blob(s, wb), max_batch=2, max_prefix=24, max_chunk=8)
+    lib, p = plain.lib, ctypes.c_void_p(256)
+    a = _abi.SvlaAdamwArgs()
+    a.state_bits, a.eps, a.step = 32, 1e-8, 1
+    assert lib.svla_train_update(plain.h, p, p, p, p, None, None, ctypes.byref(a), None, None) == _abi.SVLA_ERR_UNSUPPORTED
+    assert lib.svla_train_weights(plain.h, p, None) == _abi.SVLA_ERR_UNSUPPORTED
+    assert lib.svla_train_scale_elems(plain.h) == 0
+    plain.close()
+    m = SmolVLA(s, synth.pack_blob(s, wb), max_batch=2, max_prefix=24, max_chunk=8, train=True)
+    try:
+        master, mom = m.train_weights().float(), m.new_moments(8)
+        g = torch.zeros_like(master)
+        call = lambda **kw: lib.svla_train_update(
+            m.h, *(ctypes.c_void_p(t.data_ptr()) for t in (master, g, mom[0], mom[1])), None, None,
+            ctypes.byref(setattrs(a, **kw)), None, None)
+        setattrs = lambda x, **kw: [setattr(x, k, v) for k, v in kw.items()] and x
+        assert call(state_bits=8) == _abi.SVLA_ERR_ARG          # no scales
+        assert call(state_bits=16) == _abi.SVLA_ERR_ARG
+        assert call(state_bits=32, param_type=1) == _abi.SVLA_ERR_ARG
+        assert call(param_type=0, step=0) == _abi.SVLA_ERR_ARG
+        assert b"step" in lib.svla_last_error(m.h)
+        with pytest.raises(ValueError):
+            m.train_update(master[:-1], g, mom, 1)
+        with pytest.raises(ValueError):
+            m.train_update(master, g.to(torch.bfloat16), mom, 1)
+        with pytest.raises(_abi.SvlaError):
+            m.train_update(master, master, mom, 1)
+        with pytest.raises(ValueError):
+            m.train_weights(master)
+    finally:
+        m.close()

@@ -1,0 +1,258 @@
+"""svla_op_layernorm and its backward pass on the GPU against the oracle in float64.
+
+Tolerances. A sum of n float32 terms over a tree of depth d is off by at most
+d 2^-24 sum|terms|; a thread adds up to 32 terms in turn, then 5 shuffles and up
+to 16 warps: d <= 64. So |mean - exact| <= 64 2^-24 mean|x|, and rstd's relative
+error, half of the variance's, is at most 64 2^-24 (1 + 2 max|x| rstd ..) plus two
+units of the root: with the rows here (|x| / sigma < 8) 1e-5 covers both with a
+wide margin. y and dx are then products of a few such factors: 2e-5 of the row's
+scale, plus half a step of the output's type (bf16 2^-8 of the value). The
+column sums of dgamma and dbeta add at most M terms: M / 296 / rows-a-block of
+them in turn and then at most 64 partial ones: (M / 296 + 64) 2^-24 sum|terms|,
+beside the 2e-5 that a term of dgamma carries from xh.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import optim as oo  # noqa: E402
+from vision_language_action_b200 import _abi  # noqa: E402
+from vision_language_action_b200.runtime import AdamW, op_layernorm, op_layernorm_backward  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+DEV = "cuda:0"
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def rows(M, D, dt, gen, pad=0, scale=1.0, shift=0.0):
+    buf = torch.full((M, D + pad), 77.0, dtype=dt, device=DEV)
+    buf[:, :D] = (torch.randn(M, D, generator=gen) * scale + shift).to(dt).to(DEV)
+    return buf[:, :D]
+
+
+def make(M, D, x="f32", y="f32", w="f32", pad=0, seed=0):
+    gen = torch.Generator().manual_seed(seed * 1000 + D)
+    return dict(
+        x=rows(M, D, DT[x], gen, pad, 1.3, 0.4), dy=rows(M, D, DT[y], gen, pad, 0.1),
+        gamma=(1 + 0.3 * torch.randn(D, generator=gen)).to(DT[w]).to(DEV),
+        beta=(0.3 * torch.randn(D, generator=gen)).to(DT[w]).to(DEV),
+        y=rows(M, D, DT[y], gen, pad), dx=rows(M, D, DT[x], gen, pad),
+        mean=torch.full((M,), 9.0, device=DEV), rstd=torch.full((M,), 9.0, device=DEV),
+        dgamma=torch.full((D,), 9.0, device=DEV), dbeta=torch.full((D,), 9.0, device=DEV))
+
+
+def untouched_pad(t, pad):
+    if pad:
+        whole = t.as_strided((t.shape[0], t.shape[1] + pad), t.stride(), t.storage_offset())
+        assert (whole[:, t.shape[1]:] == 77).all()
+
+
+def check(M, D, eps=1e-5, beta=True, **kw):
+    a = make(M, D, **kw)
+    pad = kw.get("pad", 0)
+    op_layernorm(a["x"], a["gamma"], a["beta"] if beta else None, a["y"], eps, a["mean"], a["rstd"])
+    x, g, b = np64(a["x"]), np64(a["gamma"]), np64(a["beta"]) if beta else 0.0
+    y, mean, rstd = oo.layernorm(x, g, b, eps)
+    assert (np.abs(np64(a["mean"]) - mean) <= 64 * 2.0 ** -24 * np.abs(x).mean(1) + 1e-30).all()
+    if D > 1:
+        assert (np.abs(np64(a["rstd"]) / rstd - 1) <= 1e-5).all()
+    scale = np.abs((x - mean[:, None]) * rstd[:, None] * g) + 1.0
+    tol = 2e-5 * scale + HALF[a["y"].dtype] * np.abs(y) + (1e-3 if D == 1 else 0.0)
+    assert (np.abs(np64(a["y"]) - y) <= tol).all(), np.max(np.abs(np64(a["y"]) - y) / tol)
+    untouched_pad(a["y"], pad)
+    # backward, from the statistics that the forward left
+    op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"], a["rstd"], a["dx"], a["dgamma"], a["dbeta"])
+    dy = np64(a["dy"])
+    dx, dg, db = oo.layernorm_backward(dy, x, g, np64(a["mean"]), np64(a["rstd"]))
+    w = np.abs(dy * g)
+    xh = np.abs((x - np64(a["mean"])[:, None]) * np64(a["rstd"])[:, None])
+    scale = np64(a["rstd"])[:, None] * (w + w.mean(1, keepdims=True) + xh * (w * xh).mean(1, keepdims=True))
+    tol = 2e-5 * scale + HALF[a["dx"].dtype] * np.abs(dx)
+    assert (np.abs(np64(a["dx"]) - dx) <= tol).all(), np.max(np.abs(np64(a["dx"]) - dx) / tol)
+    untouched_pad(a["dx"], pad)
+    chain = (M / 296 + 64) * 2.0 ** -24
+    assert (np.abs(np64(a["dgamma"]) - dg) <= (chain + 1e-6) * (np.abs(dy) * xh).sum(0) + 1e-30).all()
+    assert (np.abs(np64(a["dbeta"]) - db) <= chain * np.abs(dy).sum(0) + 1e-30).all()
+    return a
+
+
+# each width class of the kernels: one to four units of 8 a lane of one warp, two a thread of several, shared-memory sums
+WIDTHS = [1, 2, 7, 8, 31, 32, 255, 256, 257, 512, 513, 720, 768, 960, 1000, 1024, 1025, 1283, 2048, 4096, 5000, 8192, 8193,
+          8200, 12345, 16384]
+
+
+@pytest.mark.parametrize("D", WIDTHS)
+@pytest.mark.parametrize("M", [1, 13])
+def test_widths(M, D):
+    check(M, D, seed=M)
+
+
+@pytest.mark.parametrize("D", [768, 771, 2048, 16384])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("y", ["f32", "bf16"])
+@pytest.mark.parametrize("w", ["f32", "bf16"])
+def test_types(D, x, y, w):
+    check(37, D, x=x, y=y, w=w, seed=3)
+
+
+@pytest.mark.parametrize("pad", [1, 4, 8, 24])
+@pytest.mark.parametrize("D", [64, 768, 1283, 8200])
+def test_strides(pad, D):
+    """Rows further apart than their width; the elements between them are neither read nor written."""
+    check(21, D, pad=pad, x="bf16", y="f32")
+    check(21, D, pad=pad, x="f32", y="bf16")
+
+
+@pytest.mark.parametrize("M,D", [(2, 768), (8, 768), (9, 768), (296 * 8, 768), (296 * 8 + 1, 768), (50, 720), (5001, 33),
+                                 (701, 2048), (1000, 4096), (300, 16384)])
+def test_row_counts(M, D):
+    check(M, D, seed=5)
+
+
+def test_no_beta_and_optional_outputs():
+    a = check(40, 768, beta=False)
+    y2 = torch.empty_like(a["y"])
+    op_layernorm(a["x"], a["gamma"], None, y2, 1e-5)
+    assert torch.equal(y2, a["y"])
+    for dg, db in ((None, None), (a["dgamma"].clone(), None), (None, a["dbeta"].clone())):
+        dx = torch.empty_like(a["dx"])
+        for t in (dg, db):
+            if t is not None:
+                t.fill_(5.0)
+        op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"], a["rstd"], dx, dg, db)
+        assert torch.equal(dx, a["dx"])
+        assert dg is None or torch.equal(dg, a["dgamma"])
+        assert db is None or torch.equal(db, a["dbeta"])
+
+
+def test_no_rows():
+    a = make(0, 768)
+    op_layernorm(a["x"], a["gamma"], a["beta"], a["y"], 1e-5, a["mean"], a["rstd"])
+    op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"], a["rstd"], a["dx"], a["dgamma"], a["dbeta"])
+    assert not a["dgamma"].any() and not a["dbeta"].any()
+
+
+@pytest.mark.parametrize("M,D", [(100, 768), (77, 2048), (30, 771), (20, 16384)])
+def test_in_place(M, D):
+    a = make(M, D, seed=9)
+    keep = a["x"].clone()
+    op_layernorm(a["x"], a["gamma"], a["beta"], a["y"], 1e-5, a["mean"], a["rstd"])
+    op_layernorm(keep, a["gamma"], a["beta"], keep, 1e-5)
+    assert torch.equal(keep, a["y"])
+    op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"], a["rstd"], a["dx"], a["dgamma"], a["dbeta"])
+    for over in ("x", "dy"):
+        b = {k: v.clone() for k, v in a.items()}
+        op_layernorm_backward(b["dy"], b["x"], b["gamma"], b["mean"], b["rstd"], b[over], b["dgamma"], b["dbeta"])
+        assert torch.equal(b[over], a["dx"]) and torch.equal(b["dgamma"], a["dgamma"])
+
+
+def test_constant_rows_and_large_offsets():
+    """A constant row has no variance: y is beta; a mean far from zero costs no more than the mean's own rounding."""
+    x = torch.full((5, 768), 3.0, device=DEV)
+    a = make(5, 768)
+    op_layernorm(x, a["gamma"], a["beta"], a["y"], 1e-5, a["mean"], a["rstd"])
+    assert torch.allclose(a["y"], a["beta"].expand(5, 768), atol=1e-3) and (a["mean"] - 3).abs().max() < 1e-6
+    gen = torch.Generator().manual_seed(1)
+    x = rows(6, 768, torch.float32, gen, scale=1.0, shift=1000.0)
+    op_layernorm(x, a["gamma"], a["beta"], a["y"].new_empty(6, 768), 1e-5, m := torch.empty(6, device=DEV),
+                 r := torch.empty(6, device=DEV))
+    _, mean, rstd = oo.layernorm(np64(x), 1.0, 0.0, 1e-5)
+    # the differences to a mean that is off by e add e^2 to a variance of 1: e <= 64 2^-24 1000
+    assert np.abs(np64(m) - mean).max() <= 64 * 2.0 ** -24 * 1000 and np.abs(np64(r) / rstd - 1).max() <= 2e-5
+
+
+def test_values_that_are_not_finite_stay_in_their_row():
+    for bad in (float("nan"), float("inf")):
+        for D in (768, 2048, 771):
+            a, b = make(20, D, seed=4), make(20, D, seed=4)
+            b["x"][7, 5] = bad
+            for t in (a, b):
+                op_layernorm(t["x"], t["gamma"], t["beta"], t["y"], 1e-5, t["mean"], t["rstd"])
+                op_layernorm_backward(t["dy"], t["x"], t["gamma"], t["mean"], t["rstd"], t["dx"], t["dgamma"], t["dbeta"])
+            keep = [i for i in range(20) if i != 7]
+            assert torch.equal(a["y"][keep], b["y"][keep]) and torch.equal(a["dx"][keep], b["dx"][keep])
+            assert not torch.isfinite(b["y"][7]).any() and torch.equal(a["dbeta"], b["dbeta"])
+
+
+def test_repeatable_on_another_stream_and_in_a_graph():
+    a = make(3000, 768, x="bf16", y="bf16")
+    fwd = lambda t, s=None: op_layernorm(t["x"], t["gamma"], t["beta"], t["y"], 1e-5, t["mean"], t["rstd"], stream=s)
+    bwd = lambda t, s=None: op_layernorm_backward(t["dy"], t["x"], t["gamma"], t["mean"], t["rstd"], t["dx"], t["dgamma"],
+                                                  t["dbeta"], stream=s)
+    fwd(a), bwd(a)
+    ref = {k: v.clone() for k, v in a.items()}
+    side = torch.cuda.Stream()
+    for k in ("y", "dx", "dgamma", "dbeta", "mean", "rstd"):
+        a[k].fill_(1.0)
+    torch.cuda.synchronize()
+    fwd(a, side), bwd(a, side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a[k], ref[k]) for k in ref)
+    graphs = []
+    for _ in range(2):  # each with a workspace of its own
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fwd(a), bwd(a)
+        graphs.append(g)
+    for g in graphs:
+        for k in ("y", "dx", "dgamma", "dbeta", "mean", "rstd"):
+            a[k].fill_(1.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[k], ref[k]) for k in ref)
+
+
+def test_python_refusals():
+    a = make(4, 64)
+    with pytest.raises(ValueError):
+        op_layernorm(a["x"].half(), a["gamma"], None, a["y"])
+    with pytest.raises(ValueError):
+        op_layernorm(a["x"].t(), a["gamma"], None, a["y"])
+    with pytest.raises(ValueError):
+        op_layernorm(a["x"], a["gamma"][:-1], None, a["y"])
+    with pytest.raises(ValueError):
+        op_layernorm(a["x"], a["gamma"], a["beta"].to(torch.bfloat16), a["y"])
+    with pytest.raises(ValueError):
+        op_layernorm(a["x"][:1].expand(4, 64), a["gamma"], None, a["y"])
+    with pytest.raises(ValueError):
+        op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"][:-1], a["rstd"], a["dx"])
+    with pytest.raises(ValueError):
+        op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"], a["rstd"], a["dx"].to(torch.bfloat16))
+    with pytest.raises(_abi.SvlaError):
+        op_layernorm(a["x"], a["gamma"], None, a["y"], eps=0.0)
+
+
+def test_norm_backward_and_optimiser_together():
+    """A layer norm trained as it would be: forward, backward, AdamW on gain and bias (bf16 copies that the next
+    forward reads), against the same three steps in float64."""
+    M, D = 600, 768
+    a = make(M, D, x="bf16", y="bf16", w="bf16", seed=2)
+    gain, bias = a["gamma"].float(), a["beta"].float()
+    opt = AdamW([gain, bias], lr=1e-2, weight_decay=0.0, copies=[a["gamma"], a["beta"]], max_norm=1.0)
+    x, dy = np64(a["x"]), np64(a["dy"])
+    p = [np64(gain), np64(bias)]
+    mom = [[np.zeros(D), np.zeros(D)], [np.zeros(D), np.zeros(D)]]
+    for step in range(1, 4):
+        op_layernorm(a["x"], a["gamma"], a["beta"], a["y"], 1e-5, a["mean"], a["rstd"])
+        g16 = [np64(a["gamma"]), np64(a["beta"])]
+        y, mean, rstd = oo.layernorm(x, g16[0], g16[1], 1e-5)
+        assert np.abs(np64(a["y"]) - y).max() <= 2.0 ** -8 * np.abs(y).max() + 1e-4
+        op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"], a["rstd"], a["dx"], a["dgamma"], a["dbeta"])
+        opt.step([a["dgamma"], a["dbeta"]])
+        _, dg, db = oo.layernorm_backward(dy, x, g16[0], mean, rstd)
+        c = oo.clip_factor(oo.grad_norm([dg, db]), 1.0)
+        for i, g in enumerate((dg, db)):
+            p[i], mom[i][0], mom[i][1] = oo.adamw(p[i], g, *mom[i], 1e-2, 0.9, 0.999, 1e-8, 0.0, step, c=c)
+        # m / sqrt(v) keeps the gradients' relative error (1e-6 of sum|terms|, up to 1e-3 of a sum that cancels)
+        assert np.abs(np64(gain) - p[0]).max() <= 1e-2 * step * 2e-3 and np.abs(np64(bias) - p[1]).max() <= 1e-2 * step * 2e-3
+        assert torch.equal(a["gamma"], gain.to(torch.bfloat16)) and torch.equal(a["beta"], bias.to(torch.bfloat16))

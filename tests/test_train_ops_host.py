@@ -1,0 +1,187 @@
+"""Refusals of the training operators: arguments that are wrong are rejected on
+the host, before any CUDA work (so these run without a GPU)."""
+import ctypes
+
+import pytest
+
+from vision_language_action_b200 import _abi
+
+ARG, SHAPE = _abi.SVLA_ERR_ARG, _abi.SVLA_ERR_SHAPE
+F32, BF16 = _abi.TYPE_F32, _abi.TYPE_BF16
+BASE = 1 << 40  # addresses that are never read
+
+
+def tensor(at=0, n=1000, bits=32, **kw):
+    """One tensor whose ranges lie apart from those of every other `at`."""
+    t = _abi.SvlaAdamwTensor()
+    room = BASE + at * (1 << 30)
+    for i, name in enumerate(("param", "grad", "m", "v", "copy", "m_scale", "v_scale")):
+        if bits == 8 or "scale" not in name:
+            setattr(t, name, room + i * (1 << 26))
+    t.n, t.decay = n, 1
+    for k, x in kw.items():
+        setattr(t, k, x)
+    return t
+
+
+def args(**kw):
+    a = _abi.SvlaAdamwArgs()
+    a.state_bits, a.lr, a.beta1, a.beta2, a.eps, a.weight_decay, a.step = 32, 1e-3, 0.9, 0.999, 1e-8, 0.01, 1
+    for k, x in kw.items():
+        setattr(a, k, x)
+    return a
+
+
+def adamw(ts, a, ws=None, ws_bytes=0, norm=None, n=None):
+    lib = _abi.load()
+    arr = (_abi.SvlaAdamwTensor * max(1, len(ts)))(*ts)
+    st = lib.svla_op_adamw(arr, len(ts) if n is None else n, ctypes.byref(a) if a is not None else None, ws, ws_bytes,
+                           norm, None)
+    return st, lib.svla_last_error(None).decode()
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(param_type=2), ARG), (dict(grad_type=-1), ARG), (dict(state_bits=16), ARG), (dict(lr=-1.0), ARG),
+    (dict(lr=float("nan")), ARG), (dict(lr=float("inf")), ARG), (dict(beta1=1.0), ARG), (dict(beta1=-0.1), ARG),
+    (dict(beta2=1.0), ARG), (dict(beta2=float("nan")), ARG), (dict(eps=0.0), ARG), (dict(eps=1e-60), ARG),
+    (dict(eps=1e60), ARG), (dict(weight_decay=-0.1), ARG), (dict(max_norm=-1.0), ARG),
+    (dict(max_norm=float("nan")), ARG), (dict(step=0), ARG), (dict(step=-5), ARG),
+])
+def test_adamw_settings(kw, status):
+    assert adamw([tensor()], args(**kw))[0] == status
+
+
+@pytest.mark.parametrize("bits,kw,status", [
+    (32, dict(n=-1), SHAPE), (32, dict(n=(1 << 40) + 1), SHAPE), (32, dict(param=None), ARG), (32, dict(grad=None), ARG),
+    (32, dict(m=None), ARG), (32, dict(v=None), ARG), (8, dict(m_scale=None), ARG), (8, dict(v_scale=None), ARG),
+    (32, dict(param=BASE + 2), ARG), (32, dict(m=BASE + (1 << 27) + 1), ARG), (32, dict(copy=BASE + (1 << 28) + 1), ARG),
+    (8, dict(m_scale=BASE + (5 << 26) + 2), ARG),
+])
+def test_adamw_tensors(bits, kw, status):
+    st, msg = adamw([tensor(0, bits=bits), tensor(1, bits=bits, **kw)], args(state_bits=bits))
+    assert st == status and "tensor 1" in msg
+
+
+def test_adamw_null_count_and_workspace():
+    assert adamw([], None)[0] == ARG
+    assert adamw([tensor()], args(), n=-1)[0] == ARG
+    lib = _abi.load()
+    assert lib.svla_op_adamw(None, 1, ctypes.byref(args()), None, 0, None, None) == ARG
+    need = lib.svla_op_adamw_workspace_bytes(1)
+    assert need > 0 and lib.svla_op_adamw_workspace_bytes(401) == 2 * need == lib.svla_op_adamw_workspace_bytes(800)
+    assert lib.svla_op_adamw_workspace_bytes(-1) == 0 and lib.svla_op_adamw_workspace_bytes(0) == need
+    clip = args(max_norm=1.0)
+    assert adamw([tensor()], clip)[0] == ARG
+    assert adamw([tensor()], clip, BASE - 4096 * 16, need - 1)[0] == ARG
+    assert adamw([tensor()], clip, BASE - 4096 * 16 + 4, need)[0] == ARG
+    # the empty list is a step over nothing, and so are empty tensors' pointers
+    assert adamw([], args())[0] == _abi.SVLA_OK
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("name", ["param", "m", "v", "copy", "grad", "m_scale"])
+def test_adamw_overlaps(name, bits):
+    """Memory that is written may not be listed twice, nor read through another name."""
+    if name == "m_scale" and bits == 32:
+        pytest.skip("no scales")
+    a, b = tensor(0, bits=bits), tensor(1, bits=bits)
+    # the last element of the first tensor's parameters
+    setattr(b, name, a.param + 4 * 999 if name not in ("m", "v") or bits == 32 else a.param + 3999)
+    st, msg = adamw([a, b], args(state_bits=bits))
+    assert st == ARG and "overlaps" in msg
+    assert adamw([a, a], args(state_bits=bits))[0] == ARG
+    # a tensor's own moments may not share memory either
+    c = tensor(0, bits=bits)
+    c.v = c.m
+    assert adamw([c], args(state_bits=bits))[0] == ARG
+
+
+def test_adamw_norm_and_workspace_overlaps():
+    a = tensor()
+    need = _abi.load().svla_op_adamw_workspace_bytes(1)
+    assert adamw([a], args(max_norm=1.0), a.m, need)[0] == ARG
+    assert adamw([a], args(max_norm=1.0), BASE - 4096 * 16, need, a.param)[0] == ARG
+    assert adamw([a], args(max_norm=1.0), BASE - 4096 * 16, need, a.grad + 8)[0] == ARG
+
+
+def ln(**kw):
+    """svla_op_layernorm with ranges that lie apart, and the arguments given in place of the usual ones."""
+    a = dict(x=BASE, xt=F32, ldx=64, g=BASE + (1 << 24), b=BASE + (2 << 24), wt=F32, M=10, D=64, eps=1e-5,
+             y=BASE + (3 << 24), yt=F32, ldy=64, mean=BASE + (4 << 24), rstd=BASE + (5 << 24))
+    a.update(kw)
+    return _abi.load().svla_op_layernorm(a["x"], a["xt"], a["ldx"], a["g"], a["b"], a["wt"], a["M"], a["D"], a["eps"],
+                                         a["y"], a["yt"], a["ldy"], a["mean"], a["rstd"], None)
+
+
+def ln_bwd(**kw):
+    a = dict(dy=BASE, yt=F32, lddy=64, x=BASE + (1 << 24), xt=F32, ldx=64, g=BASE + (2 << 24), wt=F32,
+             mean=BASE + (3 << 24), rstd=BASE + (4 << 24), M=1000, D=64, dx=BASE + (5 << 24), lddx=64,
+             dg=BASE + (6 << 24), db=BASE + (7 << 24), ws=BASE + (8 << 24), n=1 << 23)
+    a.update(kw)
+    return _abi.load().svla_op_layernorm_backward(
+        a["dy"], a["yt"], a["lddy"], a["x"], a["xt"], a["ldx"], a["g"], a["wt"], a["mean"], a["rstd"], a["M"], a["D"],
+        a["dx"], a["lddx"], a["dg"], a["db"], a["ws"], a["n"], None)
+
+
+COMMON = [
+    (dict(xt=2), ARG), (dict(yt=-1), ARG), (dict(wt=7), ARG), (dict(M=-1), SHAPE), (dict(D=0), SHAPE),
+    (dict(D=16385, ldx=1 << 15), SHAPE), (dict(ldx=63), SHAPE), (dict(g=None), ARG), (dict(x=None), ARG),
+    (dict(x=BASE + 2), ARG), (dict(g=BASE + (1 << 24) + 2), ARG),
+]
+
+
+@pytest.mark.parametrize("kw,status", COMMON + [
+    (dict(ldy=63), SHAPE), (dict(eps=0.0), SHAPE), (dict(eps=float("nan")), SHAPE), (dict(y=None), ARG),
+    (dict(y=BASE + (3 << 24) + 1), ARG), (dict(mean=BASE + (4 << 24) + 2), ARG),
+    # overlaps: y in x but not x itself, y over the weights or the statistics, the statistics over an input
+    (dict(y=BASE + 64 * 4), ARG), (dict(y=BASE, ldy=65), ARG), (dict(y=BASE, yt=BF16), ARG),
+    (dict(y=BASE + (1 << 24) - 2000), ARG), (dict(b=BASE + (3 << 24)), ARG), (dict(mean=BASE + (3 << 24) + 4), ARG),
+    (dict(rstd=BASE + 8), ARG), (dict(mean=BASE + (5 << 24) + 36), ARG), (dict(mean=BASE + (1 << 24) + 4), ARG),
+])
+def test_layernorm_refusals(kw, status):
+    assert ln(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", COMMON + [
+    (dict(lddy=63), SHAPE), (dict(lddx=63), SHAPE), (dict(dy=None), ARG), (dict(dx=None), ARG), (dict(mean=None), ARG),
+    (dict(rstd=None), ARG), (dict(dg=BASE + (6 << 24) + 2), ARG), (dict(ws=None), ARG), (dict(n=1000), ARG),
+    (dict(ws=BASE + (8 << 24) + 2), ARG),
+    (dict(dx=BASE + 4 * 64), ARG), (dict(dx=BASE + (1 << 24), lddx=72), ARG), (dict(dx=BASE + (2 << 24)), ARG),
+    (dict(dx=BASE + (3 << 24)), ARG), (dict(dg=BASE + (7 << 24) + 4), ARG), (dict(db=BASE + 400), ARG),
+    (dict(dg=BASE + (1 << 24)), ARG), (dict(ws=BASE + (5 << 24) + 64), ARG), (dict(db=BASE + (2 << 24) + 8), ARG),
+    (dict(dg=BASE + (8 << 24) + 16), ARG),
+])
+def test_layernorm_backward_refusals(kw, status):
+    assert ln_bwd(**kw) == status
+
+
+def test_layernorm_workspace_sizes():
+    lib = _abi.load()
+    f = lib.svla_op_layernorm_backward_workspace_bytes
+    assert f(0, 64) == f(10, 0) == f(-3, 64) == f(10, 16385) == 0
+    assert f(1, 64) == 0  # one block writes the gradients itself
+    assert f(1 << 20, 768) % (2 * 768 * 4) == 0 and f(1 << 20, 768) == f(1 << 24, 768) > 0
+    # no rows: nothing to do, and the pointers are not looked at
+    assert ln(M=0, x=None, y=None) == _abi.SVLA_OK
+
+
+def test_train_update_null_and_missing_handle():
+    lib = _abi.load()
+    p = ctypes.c_void_p(64)
+    assert lib.svla_train_update(None, p, p, p, p, None, None, ctypes.byref(args()), None, None) == ARG
+    assert lib.svla_train_weights(None, p, None) == ARG
+    assert lib.svla_train_scale_elems(None) == 0
+
+
+def test_python_face_refuses_host_tensors():
+    torch = pytest.importorskip("torch")
+    from vision_language_action_b200 import runtime as rt
+    x, g = torch.zeros(4, 64), torch.ones(64)
+    with pytest.raises(ValueError):
+        rt.op_layernorm(x, g, None, torch.empty_like(x))
+    with pytest.raises(ValueError):
+        rt.op_layernorm_backward(x, x, g, torch.zeros(4), torch.zeros(4), torch.empty_like(x))
+    with pytest.raises(ValueError):
+        rt.AdamW([x])
+    with pytest.raises(ValueError):
+        rt.AdamW([])

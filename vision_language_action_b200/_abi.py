@@ -19,6 +19,7 @@ SVLA_ERR_ARG, SVLA_ERR_SHAPE, SVLA_ERR_BLOB_SIZE = -1, -2, -3
 SVLA_ERR_EMPTY_PREFIX, SVLA_ERR_CUDA, SVLA_ERR_OOM = -4, -5, -6
 SVLA_ERR_TIMEOUT, SVLA_ERR_UNSUPPORTED = -7, -8
 
+TYPE_F32, TYPE_BF16 = 0, 1
 EPI_F32, EPI_BF16, EPI_ADD_F32, EPI_SILU_BF16 = 0, 1, 2, 3
 
 
@@ -28,6 +29,18 @@ class SvlaConfig(ctypes.Structure):
         "e_layers", "e_width", "e_heads", "e_kv_heads", "e_ffn", "action_dim")] + \
         [(n, ctypes.c_float) for n in ("rope_base", "rms_eps", "t_min_period", "t_max_period")] + \
         [(n, ctypes.c_int) for n in ("max_batch", "max_prefix", "max_chunk")]
+
+
+class SvlaAdamwTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "m", "v", "m_scale", "v_scale", "copy")] + \
+        [("n", ctypes.c_int64), ("decay", ctypes.c_int)]
+
+
+class SvlaAdamwArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("param_type", "grad_type", "state_bits")] + \
+        [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay", "max_norm")] + \
+        [("step", ctypes.c_int64), ("seed", ctypes.c_uint64),
+         ("step_device", ctypes.c_void_p), ("lr_device", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -44,6 +57,9 @@ SIGNATURES = {
     "svla_expert_weights": (_I, [_P]),
     "svla_train_step": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _I, _P, _P, _P]),
     "svla_train_grad_elems": (_S, [_P]),
+    "svla_train_update": (_I, [_P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(SvlaAdamwArgs), _P, _P]),
+    "svla_train_scale_elems": (_S, [_P]),
+    "svla_train_weights": (_I, [_P, _P, _P]),
     "svla_destroy": (_I, [_P]),
     "svla_kv_cache_bytes": (_S, [_P, _I, _I]),
     "svla_blob_bytes": (_S, [ctypes.POINTER(SvlaConfig)]),
@@ -60,6 +76,11 @@ SIGNATURES = {
     "svla_op_gemm_splits": (_I, [_I, _I, _I]),
     "svla_op_attention": (_I, [_P, _I, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _P, _I, _P]),
     "svla_op_rmsnorm": (_I, [_P, _P, _I, _I, ctypes.c_float, _P, _P]),
+    "svla_op_layernorm": (_I, [_P, _I, _I, _P, _P, _I, _I, _I, ctypes.c_float, _P, _I, _I, _P, _P, _P]),
+    "svla_op_layernorm_backward": (_I, [_P, _I, _I, _P, _I, _I, _P, _I, _P, _P, _I, _I, _P, _I, _P, _P, _P, _S, _P]),
+    "svla_op_layernorm_backward_workspace_bytes": (_S, [_I, _I]),
+    "svla_op_adamw": (_I, [ctypes.POINTER(SvlaAdamwTensor), _I, ctypes.POINTER(SvlaAdamwArgs), _P, _S, _P, _P]),
+    "svla_op_adamw_workspace_bytes": (_S, [_I]),
     "svla_set_wait_limit_ns": (None, [ctypes.c_uint64]),
     "svla_set_denoise_path": (_I, [_P, _I]),
     "svla_assembly_blob_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),

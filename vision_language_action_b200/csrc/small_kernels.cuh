@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "philox.cuh"
 
 namespace svla {
 
@@ -357,21 +358,6 @@ __global__ void __launch_bounds__(256) step_end_kernel(const StepEndArgs p) {
 // Gaussian noise (reading 15): Philox4x32-10 (Salmon et al., SC'11), key =
 // seed, counter = (block, query, 0, 0), Box–Muller on (r0, r1) and (r2, r3).
 // ---------------------------------------------------------------------------
-SVLA_DEV void philox4x32_10(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
-#pragma unroll
-  for (int r = 0; r < 10; ++r) {
-    const uint32_t lo0 = 0xD2511F53u * c[0], hi0 = __umulhi(0xD2511F53u, c[0]);
-    const uint32_t lo1 = 0xCD9E8D57u * c[2], hi1 = __umulhi(0xCD9E8D57u, c[2]);
-    const uint32_t n0 = hi1 ^ c[1] ^ k0, n2 = hi0 ^ c[3] ^ k1;
-    c[0] = n0;
-    c[1] = lo1;
-    c[2] = n2;
-    c[3] = lo0;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
-  }
-}
-
 __global__ void philox_noise_kernel(unsigned long long seed, int B, int n_el, float* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();

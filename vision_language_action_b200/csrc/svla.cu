@@ -13,6 +13,7 @@
 #include <cstring>
 #include <algorithm>
 #include <atomic>
+#include <exception>
 #include <list>
 #include <utility>
 #include <mutex>
@@ -190,6 +191,16 @@ __global__ void bf16_to_f32_kernel(const uint16_t* __restrict__ src, float* __re
   if (i < n) dst[i] = __uint_as_float(((uint32_t)src[i]) << 16);
 }
 
+// the same for the two biases of the training step that it reads in fp32
+__global__ void train_biases_kernel(const uint16_t* __restrict__ b1, const uint16_t* __restrict__ b2,
+                                    float* __restrict__ f1, float* __restrict__ f2, int n) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < n) {
+    f1[i] = __uint_as_float(((uint32_t)b1[i]) << 16);
+    f2[i] = __uint_as_float(((uint32_t)b2[i]) << 16);
+  }
+}
+
 // Offsets (elements) of the persistent kernel's padded weight copy.
 struct FusedWeights {
   std::vector<size_t> qkv, o, gu, d;
@@ -275,12 +286,13 @@ struct TrainWs {
   float *r = nullptr, *rm = nullptr, *gu = nullptr;
   uint16_t *y = nullptr, *y2 = nullptr, *q = nullptr, *k = nullptr, *v = nullptr, *o = nullptr, *hs = nullptr;
   float *xt = nullptr, *aemb = nullptr, *z1 = nullptr, *yf = nullptr, *dv = nullptr, *loss_row = nullptr;
-  float *dyf = nullptr, *b_t1f = nullptr;
+  float *dyf = nullptr, *b_t1f = nullptr, *b_t2f = nullptr;
   uint16_t *cat = nullptr, *h1 = nullptr;
   // backward
   float *dr = nullptr, *dx = nullptr, *dz = nullptr, *rs = nullptr, *P = nullptr, *dS = nullptr;
   uint16_t *drb = nullptr, *dgu = nullptr, *dqkv = nullptr, *dkx = nullptr, *dvx = nullptr, *dob = nullptr;
   uint16_t *wt = nullptr, *ta = nullptr, *tb = nullptr;
+  uint8_t* opt_ws = nullptr;  // the clip's partial sums (svla_train_update)
 };
 
 struct GraphEntry {
@@ -591,7 +603,7 @@ cudaError_t record_train(svla_handle* h, const void* kv, const uint8_t* pad, int
                       TW(Ly.b_in.off), (const double*)h->inv_period, T.xt, T.aemb, T.cat));
   SVLA_TRY(mm(GE_F32, T.cat, 2 * E, TW(Ly.w_t1.off), 2 * E, M, E, 2 * E, out_args(T.z1, E, T.b_t1f)));
   SVLA_TRY(launch_pdl(silu_fwd_kernel, ew((size_t)M * E), dim3(256), 0, s, (const float*)T.z1, (size_t)M * E, T.h1));
-  SVLA_TRY(mm(GE_F32, T.h1, E, TW(Ly.w_t2.off), E, M, E, E, out_args(R(0), E, h->b_t2_f32)));
+  SVLA_TRY(mm(GE_F32, T.h1, E, TW(Ly.w_t2.off), E, M, E, E, out_args(R(0), E, T.b_t2f)));
   for (int l = 0; l < c.e_layers; ++l) {
     const Entry* e = &Ly.e[9 * l];
     SVLA_TRY(rmsnorm(R(l), false, nullptr, bf(TW(e[0].off)), M, E, c.rms_eps, reinterpret_cast<bf16*>(Y(l)), s));
@@ -747,6 +759,15 @@ cudaError_t record_train(svla_handle* h, const void* kv, const uint8_t* pad, int
   return cudaSuccess;
 }
 
+// the time MLP's biases in fp32, from the training weights as they are
+cudaError_t train_biases(svla_handle* h, cudaStream_t s) {
+  const TrainWs& T = *h->tr;
+  const int E = h->cfg.e_width;
+  train_biases_kernel<<<(E + 255) / 256, 256, 0, s>>>(T.tw + (h->lay.b_t1.off - T.base),
+                                                     T.tw + (h->lay.b_t2.off - T.base), T.b_t1f, T.b_t2f, E);
+  return cudaGetLastError();
+}
+
 // Allocate the training workspace (after the weights and tw are in place).
 cudaError_t alloc_train(svla_handle* h) {
   const svla_config& c = h->cfg;
@@ -779,6 +800,7 @@ cudaError_t alloc_train(svla_handle* h) {
   al(&T.loss_row, Me);
   al(&T.dyf, Me * E);
   al(&T.b_t1f, E);
+  al(&T.b_t2f, E);
   al(&T.cat, Me * 2 * E);
   al(&T.h1, Me * E);
   const size_t maxw = std::max({2 * F, qkvw, 2 * E});
@@ -800,11 +822,8 @@ cudaError_t alloc_train(svla_handle* h) {
   const size_t maxc = std::max({2 * F, qkvw, 2 * E, F, qw, pkvw, kvw, E});
   al(&T.ta, maxc * std::max(Mp, Lp));
   al(&T.tb, maxc * std::max(Mp, Lp));
-  if (e == cudaSuccess) {
-    bf16_to_f32_kernel<<<(unsigned)((E + 255) / 256), 256>>>(T.tw + (h->lay.b_t1.off - T.base), T.b_t1f, (int)E);
-    e = cudaGetLastError();
-  }
-  return e;
+  al(&T.opt_ws, svla_op_adamw_workspace_bytes(9 * c.e_layers + 9));
+  return e == cudaSuccess ? train_biases(h, nullptr) : e;
 }
 
 // ---- prefill schedule -------------------------------------------------------
@@ -1714,6 +1733,84 @@ svla_status svla_train_step(svla_handle* h, const void* kv_cache, const uint8_t*
         return record_train(h, kv_cache, pad_mask, B, L, actions, noise, t, H, loss, grads, cs);
       },
       reinterpret_cast<cudaStream_t>(stream), "train step");
+}
+
+// The expert's tensors in manifest order, with whether they are matrices.
+static std::vector<std::pair<Entry, bool>> train_tensors(const svla_handle* h) {
+  const Layout& L = h->lay;
+  std::vector<std::pair<Entry, bool>> t;
+  for (size_t i = 0; i < L.e.size(); ++i) t.push_back({L.e[i], i % 9 != 0 && i % 9 != 5});  // not the two norms' gains
+  for (const auto& x : {std::pair<Entry, bool>{L.final_norm, false}, {L.w_in, true}, {L.b_in, false}, {L.w_t1, true},
+                        {L.b_t1, false}, {L.w_t2, true}, {L.b_t2, false}, {L.w_out, true}, {L.b_out, false}})
+    t.push_back(x);
+  return t;
+}
+
+size_t svla_train_scale_elems(const svla_handle* h) {
+  if (!h || !h->tr) return 0;
+  size_t n = 0;
+  try {
+    for (const auto& t : train_tensors(h)) n += (t.first.n + 255) / 256;
+  } catch (const std::exception&) {
+    return 0;
+  }
+  return n;
+}
+
+svla_status svla_train_update(svla_handle* h, float* master, const float* grads, void* m, void* v, float* m_scale,
+                              float* v_scale, const svla_adamw_args* args, float* grad_norm, void* stream) {
+  if (!h) return fail(nullptr, SVLA_ERR_ARG, "null handle");
+  if (!master || !grads || !m || !v || !args) return fail(h, SVLA_ERR_ARG, "null pointer");
+  if (!h->tr) return fail(h, SVLA_ERR_UNSUPPORTED, "the handle has no training workspace (create it with SVLA_CREATE_TRAIN)");
+  if (args->param_type != SVLA_TYPE_F32 || args->grad_type != SVLA_TYPE_F32)
+    return fail(h, SVLA_ERR_ARG, "master weights and gradients are float32");
+  if (args->state_bits != 32 && args->state_bits != 8) return fail(h, SVLA_ERR_ARG, "state_bits must be 32 or 8");
+  if (args->state_bits == 8 && (!m_scale || !v_scale)) return fail(h, SVLA_ERR_ARG, "8-bit states need m_scale and v_scale");
+  const TrainWs& T = *h->tr;
+  DeviceGuard dg(h->device);
+  try {
+    std::vector<svla_adamw_tensor> ts;
+    size_t scale_at = 0;
+    for (const auto& t : train_tensors(h)) {
+      const size_t at = t.first.off - T.base, state_bytes = args->state_bits / 8;
+      svla_adamw_tensor a = {};
+      a.param = master + at;
+      a.grad = grads + at;
+      a.m = static_cast<uint8_t*>(m) + at * state_bytes;
+      a.v = static_cast<uint8_t*>(v) + at * state_bytes;
+      if (args->state_bits == 8) {
+        a.m_scale = m_scale + scale_at;
+        a.v_scale = v_scale + scale_at;
+      }
+      a.copy = T.tw + at;
+      a.n = (int64_t)t.first.n;
+      a.decay = t.second;
+      ts.push_back(a);
+      scale_at += (t.first.n + 255) / 256;
+    }
+    if (svla_status st = svla_op_adamw(ts.data(), (int)ts.size(), args, T.opt_ws,
+                                       svla_op_adamw_workspace_bytes((int)ts.size()), grad_norm, stream);
+        st != SVLA_OK) {
+      h->last_error = t_last_error;
+      return st;
+    }
+  } catch (const std::exception&) {
+    return fail(h, SVLA_ERR_OOM, "out of host memory");
+  }
+  if (cudaError_t e = train_biases(h, reinterpret_cast<cudaStream_t>(stream)); e != cudaSuccess)
+    return cuda_fail(h, e, "train update");
+  return SVLA_OK;
+}
+
+svla_status svla_train_weights(svla_handle* h, void* out, void* stream) {
+  if (!h) return fail(nullptr, SVLA_ERR_ARG, "null handle");
+  if (!out) return fail(h, SVLA_ERR_ARG, "null pointer");
+  if (!h->tr) return fail(h, SVLA_ERR_UNSUPPORTED, "the handle has no training workspace (create it with SVLA_CREATE_TRAIN)");
+  DeviceGuard dg(h->device);
+  const cudaError_t e = cudaMemcpyAsync(out, h->tr->tw, svla_train_grad_elems(h) * 2, cudaMemcpyDeviceToDevice,
+                                        reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(h, e, "train weights");
+  return SVLA_OK;
 }
 
 int svla_denoise_fused_supported(const svla_handle* h, int B, int H) {

@@ -6,13 +6,13 @@ to own device memory and to name the current CUDA stream.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from typing import List, Optional, Sequence, Tuple
 
 import torch
 
 from . import _abi
 
-__all__ = ["SmolVLA", "config_from_shape"]
+__all__ = ["SmolVLA", "AdamW", "config_from_shape"]
 
 
 def config_from_shape(shape, max_batch: int, max_prefix: int, max_chunk: int) -> _abi.SvlaConfig:
@@ -200,6 +200,53 @@ class SmolVLA:
         _abi.check(st, self.h)
         return loss, grads
 
+    def train_weights(self, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The expert and head weights that the next ``train_step`` reads, bf16 in the gradients' order."""
+        n = int(self.lib.svla_train_grad_elems(self.h))
+        if out is None:
+            out = torch.empty(n, dtype=torch.bfloat16, device=f"cuda:{self.device}")
+            if stream is not None:
+                out.record_stream(stream)
+        elif out.dtype != torch.bfloat16 or out.numel() != n:
+            raise ValueError(f"out: {n} bfloat16 elements expected")
+        _abi.check(self.lib.svla_train_weights(self.h, _ptr(out), _stream(stream)), self.h)
+        return out
+
+    def new_moments(self, state_bits: int = 32):
+        """Zero moments for ``train_update``: (m, v, m_scale, v_scale), the scales None with 32 bits."""
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        n, dev = int(self.lib.svla_train_grad_elems(self.h)), f"cuda:{self.device}"
+        if state_bits == 32:
+            return torch.zeros(n, device=dev), torch.zeros(n, device=dev), None, None
+        k = int(self.lib.svla_train_scale_elems(self.h))
+        return (torch.zeros(n, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn),
+                torch.zeros(n, dtype=torch.uint8, device=dev).view(torch.float8_e5m2),
+                torch.zeros(k, device=dev), torch.zeros(k, device=dev))
+
+    def train_update(self, master: torch.Tensor, grads: torch.Tensor, moments, step: int, lr: float = 1e-4,
+                     betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 1e-2,
+                     max_norm: float = 0.0, seed: int = 0, grad_norm: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+        """One AdamW step on the float32 ``master`` weights (``train_weights`` in float32 to start with) from
+        ``train_step``'s gradients; the next ``train_step`` reads their bf16 rounding. ``moments`` as from
+        ``new_moments``, ``step`` counts from 1, ``max_norm`` > 0 clips by the global norm (into ``grad_norm``)."""
+        m, v, ms, vs = moments
+        n, k = int(self.lib.svla_train_grad_elems(self.h)), int(self.lib.svla_train_scale_elems(self.h))
+        bits = 32 if m.dtype == torch.float32 else 8
+        kinds = (torch.float32, torch.float32) if bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
+        a = _abi.SvlaAdamwArgs()
+        a.param_type = a.grad_type = _abi.TYPE_F32
+        a.state_bits, a.lr, (a.beta1, a.beta2), a.eps = bits, lr, betas, eps
+        a.weight_decay, a.max_norm, a.step, a.seed = weight_decay, max_norm, step, seed
+        st = self.lib.svla_train_update(
+            self.h, _vec(master, n, "master", torch.float32), _vec(grads, n, "grads", torch.float32),
+            _vec(m, n, "m", kinds[0]), _vec(v, n, "v", kinds[1]),
+            _vec(ms, k, "m_scale", torch.float32) if bits == 8 else None,
+            _vec(vs, k, "v_scale", torch.float32) if bits == 8 else None, ctypes.byref(a),
+            _vec(grad_norm, 1, "grad_norm", torch.float32), _stream(stream))
+        _abi.check(st, self.h)
+
     def set_prefix_weights(self, bits: int) -> None:
         """16 = dense bf16 prefix weights, 8 = the int8 copy (needs prefix_int8=True)."""
         _abi.check(self.lib.svla_set_prefix_weights(self.h, bits), self.h)
@@ -288,3 +335,209 @@ def op_rmsnorm(x: torch.Tensor, g: torch.Tensor, y: torch.Tensor, eps: float = 1
     M, D = x.shape
     _abi.check(lib.svla_op_rmsnorm(_ptr(x), _ptr(g), M, D, eps, _ptr(y), _stream(stream)))
     return y
+
+
+# ----------------------------------------------------------------------
+# training operators
+# ----------------------------------------------------------------------
+_TYPES = {torch.float32: _abi.TYPE_F32, torch.bfloat16: _abi.TYPE_BF16}
+
+
+def _type(t: torch.Tensor, what: str) -> int:
+    if t.dtype not in _TYPES:
+        raise ValueError(f"{what}: float32 or bfloat16 expected, got {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def _rows(t: torch.Tensor, shape, what: str):
+    """(pointer, type, row stride) of a [M, D] CUDA matrix whose rows are contiguous."""
+    if not t.is_cuda or tuple(t.shape) != tuple(shape) or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a CUDA matrix of shape {tuple(shape)} with contiguous rows expected")
+    ld = t.stride(0) if shape[0] > 1 else shape[1]
+    if ld < shape[1]:
+        raise ValueError(f"{what}: rows overlap")
+    return ctypes.c_void_p(t.data_ptr()), _type(t, what), ld
+
+
+def _vec(t: Optional[torch.Tensor], n: int, what: str, dtype: Optional[torch.dtype] = None):
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous() or t.numel() != n or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what}: a contiguous CUDA tensor of {n} {dtype or 'float32 or bfloat16'} elements expected")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _same_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    if any(o is not None and o.device != first.device for o in others):
+        raise ValueError("tensors are on different devices")
+
+
+def _scratch(nbytes: int, device, stream) -> Optional[torch.Tensor]:
+    """A workspace of one call; where the call runs on a stream other than the current one, the allocator is told."""
+    if nbytes == 0:
+        return None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def op_layernorm(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor], y: torch.Tensor,
+                 eps: float = 1e-5, mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """svla_op_layernorm: y = (x - mean) rstd gamma + beta over rows [M, D], float32 or bfloat16 each, any row
+    stride; ``mean`` and ``rstd`` (float32 [M]) receive the statistics that ``op_layernorm_backward`` reads."""
+    lib = _abi.load()
+    if x.dim() != 2:
+        raise ValueError("x: a [M, D] matrix expected")
+    M, D = x.shape
+    px, tx, ldx = _rows(x, (M, D), "x")
+    py, ty, ldy = _rows(y, (M, D), "y")
+    _same_device(x, gamma, beta, y, mean, rstd)
+    tw = _type(gamma, "gamma")
+    with torch.cuda.device(x.device):
+        _abi.check(lib.svla_op_layernorm(px, tx, ldx, _vec(gamma, D, "gamma"), _vec(beta, D, "beta", gamma.dtype), tw,
+                                         M, D, eps, py, ty, ldy, _vec(mean, M, "mean", torch.float32),
+                                         _vec(rstd, M, "rstd", torch.float32), _stream(stream)))
+    return y
+
+
+def op_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, mean: torch.Tensor,
+                          rstd: torch.Tensor, dx: torch.Tensor, dgamma: Optional[torch.Tensor] = None,
+                          dbeta: Optional[torch.Tensor] = None, stream=None):
+    """svla_op_layernorm_backward: writes dx (x's type) and, where given, the float32 gradients dgamma and dbeta."""
+    lib = _abi.load()
+    if x.dim() != 2:
+        raise ValueError("x: a [M, D] matrix expected")
+    M, D = x.shape
+    px, tx, ldx = _rows(x, (M, D), "x")
+    pdy, ty, lddy = _rows(dy, (M, D), "dy")
+    pdx, tdx, lddx = _rows(dx, (M, D), "dx")
+    if tdx != tx:
+        raise ValueError("dx must have x's type")
+    _same_device(x, dy, gamma, mean, rstd, dx, dgamma, dbeta)
+    tw = _type(gamma, "gamma")
+    with torch.cuda.device(x.device):
+        n = int(lib.svla_op_layernorm_backward_workspace_bytes(M, D)) if dgamma is not None or dbeta is not None else 0
+        ws = _scratch(n, x.device, stream)
+        _abi.check(lib.svla_op_layernorm_backward(
+            pdy, ty, lddy, px, tx, ldx, _vec(gamma, D, "gamma"), tw, _vec(mean, M, "mean", torch.float32),
+            _vec(rstd, M, "rstd", torch.float32), M, D, pdx, lddx, _vec(dgamma, D, "dgamma", torch.float32),
+            _vec(dbeta, D, "dbeta", torch.float32), _ptr(ws), n, _stream(stream)))
+    return dx, dgamma, dbeta
+
+
+class AdamW:
+    """svla_op_adamw over a list of parameter tensors (float32 or bfloat16, all one type, updated in place).
+
+    ``state_bits`` 32 keeps the moments in float32, 8 in float8_e4m3fn (m) and float8_e5m2 (v) with one float32
+    scale for 256 elements, stochastically rounded from ``seed``. ``max_norm`` > 0 clips by the norm over all
+    gradients (left in ``grad_norm``, float32 [1], by every step; a step whose norm is not finite changes nothing
+    else). ``copies`` (bfloat16, one a parameter) receive the updated parameters rounded. ``decay`` says for each
+    parameter whether ``weight_decay`` applies (default: to all). ``state`` = (m, v, m_scale, v_scale), lists of
+    tensors (the scales None with 32 bits), resumes with those moments and ``step`` with that many steps taken.
+    ``capturable`` counts the steps on the device, so that a captured ``step`` counts on at every replay; ``lr``
+    may then be a float64 CUDA tensor of one element, read at every step.
+    """
+
+    def __init__(self, params: Sequence[torch.Tensor], lr=1e-3, betas: Tuple[float, float] = (0.9, 0.999),
+                 eps: float = 1e-8, weight_decay: float = 1e-2, state_bits: int = 32, max_norm: float = 0.0,
+                 copies: Optional[Sequence[Optional[torch.Tensor]]] = None, decay: Optional[Sequence[bool]] = None,
+                 seed: int = 0, step: int = 0, state=None, capturable: bool = False):
+        self.lib = _abi.load()
+        self.params: List[torch.Tensor] = list(params)
+        n = len(self.params)
+        if n == 0:
+            raise ValueError("no parameters")
+        dev, dt = self.params[0].device, self.params[0].dtype
+        for p in self.params:
+            if not p.is_cuda or p.device != dev or p.dtype != dt or not p.is_contiguous():
+                raise ValueError("parameters: contiguous CUDA tensors of one type on one device expected")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        self.device, self.state_bits, self.lr, self.steps = dev, state_bits, lr, int(step)
+        size = [p.numel() for p in self.params]
+        if state is None:
+            # one buffer a moment; every tensor's part starts on 16 bytes
+            unit = 4 if state_bits == 32 else 16
+            at = [0]
+            for k in size:
+                at.append(at[-1] + (k + unit - 1) // unit * unit)
+            kinds = ((torch.float32,) * 2) if state_bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
+            flat = [torch.zeros(at[-1] * (4 if state_bits == 32 else 1), dtype=torch.uint8, device=dev).view(k)
+                    for k in kinds]
+            self.m, self.v = ([f[a:a + k] for a, k in zip(at, size)] for f in flat)
+            self.m_scale = self.v_scale = None
+            if state_bits == 8:
+                per = [(k + 255) // 256 for k in size]
+                self.m_scale = list(torch.zeros(sum(per), device=dev).split(per))
+                self.v_scale = list(torch.zeros(sum(per), device=dev).split(per))
+        else:
+            self.m, self.v, self.m_scale, self.v_scale = (None if x is None else list(x) for x in state)
+            kinds = ((torch.float32,) * 2) if state_bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
+            for i, k in enumerate(size):
+                for what, x, d, c in (("m", self.m[i], kinds[0], k), ("v", self.v[i], kinds[1], k)) + (
+                        () if state_bits == 32 else (("m_scale", self.m_scale[i], torch.float32, (k + 255) // 256),
+                                                     ("v_scale", self.v_scale[i], torch.float32, (k + 255) // 256))):
+                    _vec(x, c, f"{what} of parameter {i}", d)
+                    _same_device(self.params[0], x)
+        self.copies = [None] * n if copies is None else list(copies)
+        flags = [True] * n if decay is None else [bool(d) for d in decay]
+        if len(self.copies) != n or len(flags) != n or len(self.m) != n or len(self.v) != n:
+            raise ValueError("copies, decay and state must have one entry a parameter")
+        self._size, self._grad_type = size, None
+        self._table = (_abi.SvlaAdamwTensor * n)()
+        for i, e in enumerate(self._table):
+            e.param, e.m, e.v, e.n, e.decay = self.params[i].data_ptr(), self.m[i].data_ptr(), self.v[i].data_ptr(), \
+                size[i], int(flags[i])
+            if state_bits == 8:
+                e.m_scale, e.v_scale = self.m_scale[i].data_ptr(), self.v_scale[i].data_ptr()
+            if self.copies[i] is not None:
+                _vec(self.copies[i], size[i], f"copy of parameter {i}", torch.bfloat16)
+                _same_device(self.params[0], self.copies[i])
+                e.copy = self.copies[i].data_ptr()
+        self.capturable = capturable
+        self.step_tensor = torch.full((1,), self.steps, dtype=torch.int64, device=dev) if capturable else None
+        if isinstance(lr, torch.Tensor) and (not capturable or lr.dtype != torch.float64 or lr.device != dev
+                                             or lr.numel() != 1):
+            raise ValueError("a tensor lr: one float64 on the parameters' device, with capturable")
+        self.grad_norm = torch.zeros(1, device=dev) if max_norm else None
+        ws = int(self.lib.svla_op_adamw_workspace_bytes(n)) if max_norm else 0
+        self._ws = torch.empty(ws, dtype=torch.uint8, device=dev) if ws else None
+        a = self._args = _abi.SvlaAdamwArgs()
+        a.param_type, a.state_bits = _type(self.params[0], "parameters"), state_bits
+        (a.beta1, a.beta2), a.eps, a.weight_decay, a.max_norm, a.seed = betas, eps, weight_decay, max_norm, seed
+
+    def step(self, grads: Sequence[torch.Tensor], lr: Optional[float] = None, stream=None) -> None:
+        """One step with these gradients (float32 or bfloat16, all one type, one contiguous tensor a parameter)."""
+        if len(grads) != len(self._size):
+            raise ValueError(f"{len(self._size)} gradients expected, got {len(grads)}")
+        dt = grads[0].dtype
+        for g, k, e in zip(grads, self._size, self._table):
+            if g.dtype != dt or g.device != self.device or g.numel() != k or not g.is_contiguous():
+                raise ValueError("gradients: contiguous tensors of one type and the parameters' sizes, on their device")
+            e.grad = g.data_ptr()
+        a = self._args
+        a.grad_type = _type(grads[0], "gradients")
+        rate = self.lr if lr is None else lr
+        with torch.cuda.device(self.device):
+            if self.capturable:
+                on = stream if stream is not None else torch.cuda.current_stream()
+                with torch.cuda.stream(on):
+                    self.step_tensor.add_(1)
+                a.step_device = self.step_tensor.data_ptr()
+                a.step = 1
+            else:
+                a.step = self.steps + 1
+            if isinstance(rate, torch.Tensor):
+                a.lr, a.lr_device = 0.0, rate.data_ptr()
+            else:
+                a.lr, a.lr_device = float(rate), None
+            st = self.lib.svla_op_adamw(self._table, len(self._size), ctypes.byref(a), _ptr(self._ws),
+                                        0 if self._ws is None else self._ws.numel(), _ptr(self.grad_norm),
+                                        _stream(stream))
+            if st != _abi.SVLA_OK and self.capturable:
+                with torch.cuda.stream(on):
+                    self.step_tensor.sub_(1)
+            _abi.check(st)
+        self.steps += 1
