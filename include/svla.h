@@ -210,7 +210,7 @@ typedef struct svla_adamw_args {
  *     matrices, not to gains and biases. The tensor index is the tensor's place
  *     among the gradients (0 for the first expert layer's in_norm).
  *   grad_norm: with a clip, device float32 scalar or NULL.
- * 16-byte aligned buffers (8 for 8-bit codes) take wide accesses. The weights of
+ * Buffers aligned to 8 elements (32 bytes for float32) take wide accesses. The weights of
  * svla_prefill, svla_denoise and svla_sample stay those given at creation: a
  * handle for them is created from the updated weights. Stream-ordered; needs a
  * handle created with SVLA_CREATE_TRAIN (else SVLA_ERR_UNSUPPORTED). */
@@ -467,8 +467,8 @@ SVLA_API size_t svla_op_layernorm_backward_workspace_bytes(int M, int D);
 
 /* One AdamW step over many tensors, in place: the update that follows
  * svla_train_step ("noeira docs, SmolVLA" §Fine-tuning), for any list of
- * tensors (svla_train_update takes the expert's). Per element, each product
- * and sum rounded to fp32, t the step number:
+ * tensors (svla_train_update takes the expert's). Per element, in fp32 (the
+ * moments' products and sums each rounded by themselves), t the step number:
  *   g' = c g,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
  *   p  = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * (weight_decay only where the tensor's `decay` is set), then copy = bf16(p).
@@ -491,8 +491,8 @@ SVLA_API size_t svla_op_layernorm_backward_workspace_bytes(int M, int D);
  *   Zero bytes are a valid start (all moments 0).
  * The device pointers and n of all tensors; the table is read during the call
  * only. n = 0 is skipped. Pointers need their element type's alignment;
- * tensors whose pointers are all 16-byte aligned (8 for 8-bit codes) are read
- * in wide accesses. Memory that is written may not overlap any other range of
+ * tensors whose pointers are all aligned to 8 elements (32 bytes for float32,
+ * 16 for bf16, 8 for codes) are read in wide accesses. Memory that is written may not overlap any other range of
  * the call (SVLA_ERR_ARG), so no tensor may be listed twice; gradients may be
  * shared.
  *   step_device, lr_device: NULL, or a device int64 / double read when the step

@@ -3,17 +3,16 @@
 // gradient norm. The update half of the expert's fine-tune, whose loss and
 // gradients svla_train_step computes.
 //
-// Per element, every product and sum rounded to fp32 by itself (no fused
-// multiply-add), so the stored moments do not depend on how the compiler
+// Per element, the moments' products and sums rounded to fp32 one by one (no
+// fused multiply-add), so what is stored does not depend on how the compiler
 // contracts the expression:
 //   g' = g c,  m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2,
 //   p  = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 //
 // The tensors' table travels in the kernel's parameters: nothing is copied to
 // the device and nothing is kept between calls. A warp takes 256 consecutive
-// elements of one tensor, the block that shares a scale in the 8-bit states;
-// lanes hold 8 consecutive elements (16- and 32-byte accesses) where every
-// pointer of the tensor allows it, else every 32nd one.
+// elements of one tensor, the block that shares a scale in the 8-bit states, 8
+// consecutive ones a lane.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -63,6 +62,7 @@ struct AdamwCoefs {
   float keep;       // 1 - lr wd
   float step_size;  // lr / (1 - b1^t)
   float isb2;       // 1 / sqrt(1 - b2^t)
+  float minus0;     // -0 (product2)
   double max_norm;  // 0: no clip
   uint32_t k0, k1, step, tensor0;
   // read on the device instead of the host's numbers, where given
@@ -84,46 +84,235 @@ SVLA_DEV int find_tensor(const AdamwTable& t, uint32_t blk) {
   return lo;
 }
 
-// two 8-bit codes -> two floats (exact; through fp16, which holds both formats)
-template <bool E5M2>
-SVLA_DEV float2 decode2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, E5M2 ? __NV_E5M2 : __NV_E4M3);
+// Two fp32 values in one register pair: the packed operations round each half
+// like the scalar ones and take half the issue slots.
+typedef unsigned long long f32x2;
+SVLA_DEV f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+SVLA_DEV float2 halves(f32x2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+SVLA_DEV f32x2 both(float x) { return pair(x, x); }
+SVLA_DEV f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+SVLA_DEV f32x2 mul2_ftz(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+SVLA_DEV f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+SVLA_DEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A product that is rounded before it is added to: the compiler fuses a packed
+// product and sum even where both are .rn, but not two fused operations. The
+// addend -0 changes no product; it comes from the kernel's arguments, so that
+// the compiler does not know it.
+SVLA_DEV f32x2 product2(f32x2 a, f32x2 b, f32x2 minus0) { return fma2(a, b, minus0); }
+
+// two 8-bit codes -> two floats (exact; through fp16, which holds both formats:
+// an e5m2 code is the upper byte of its fp16 value)
+SVLA_DEV float2 decode_m2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+template <int K>
+SVLA_DEV float2 decode_v2(uint32_t four) {
+  const uint32_t h = __byte_perm(four, 0, K ? 0x3424 : 0x1404);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// two values that the formats hold -> their codes (lo in the low byte)
+SVLA_DEV uint32_t code_m2(f32x2 x) {
+  uint16_t r;
+  const float2 f = halves(x);
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(f.y), "f"(f.x));
+  return r;
+}
+SVLA_DEV uint32_t code_v2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 8 elements of this lane from a warp's 256, raw, packed into words. `vec`: the
+// consecutive elements lane * 8 .., one 32-byte (fp32), 16-byte (bf16) or 8-byte
+// (codes) access; else (a tensor's last, shorter block, or a tensor at an odd
+// address) the elements lane, lane + 32, .., zeros past the tensor's end.
+template <typename E>
+struct Raw8 {
+  uint32_t w[2 * sizeof(E)];
+};
+template <typename E>
+SVLA_DEV void raw_load(const E* p, bool vec, int left, int lane, Raw8<E>& r) {
+  if (vec) {
+    if constexpr (sizeof(E) == 4) {
+      ld_global_v8(p + lane * 8, r.w);
+    } else if constexpr (sizeof(E) == 2) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p + lane * 8);
+      r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
+    } else {
+      const uint2 q = *reinterpret_cast<const uint2*>(p + lane * 8);
+      r.w[0] = q.x, r.w[1] = q.y;
+    }
+    return;
+  }
+  uint32_t x[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (sizeof(E) == 4)
+      x[j] = j * 32 + lane < left ? __float_as_uint(p[j * 32 + lane]) : 0u;
+    else
+      x[j] = j * 32 + lane < left ? p[j * 32 + lane] : 0u;
+  }
+  constexpr int PER = 4 / sizeof(E);  // elements of a word
+#pragma unroll
+  for (int k = 0; k < 8 / PER; ++k) {
+    r.w[k] = x[PER * k];
+#pragma unroll
+    for (int q = 1; q < PER; ++q) r.w[k] |= x[PER * k + q] << (8 * sizeof(E) * q);
+  }
+}
+template <typename E>
+SVLA_DEV void raw_store(E* p, bool vec, int left, int lane, const Raw8<E>& r) {
+  if (vec) {
+    if constexpr (sizeof(E) == 4)
+      st_global_v8(p + lane * 8, r.w);
+    else if constexpr (sizeof(E) == 2)
+      *reinterpret_cast<uint4*>(p + lane * 8) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    else
+      *reinterpret_cast<uint2*>(p + lane * 8) = make_uint2(r.w[0], r.w[1]);
+    return;
+  }
+  constexpr int PER = 4 / sizeof(E);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j * 32 + lane < left) {
+      const uint32_t x = r.w[j / PER] >> (8 * sizeof(E) * (j % PER));
+      if constexpr (sizeof(E) == 4)
+        p[j * 32 + lane] = __uint_as_float(x);
+      else
+        p[j * 32 + lane] = (E)x;
+    }
+}
+SVLA_DEV float value(const Raw8<float>& r, int j) { return __uint_as_float(r.w[j]); }
+SVLA_DEV float value(const Raw8<uint16_t>& r, int j) {
+  return __uint_as_float((j & 1) ? (r.w[j >> 1] & 0xffff0000u) : (r.w[j >> 1] << 16));
+}
+SVLA_DEV void pack(const float (&x)[8], Raw8<float>& r) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r.w[j] = __float_as_uint(x[j]);
+}
+SVLA_DEV void pack(const float (&x)[8], Raw8<uint16_t>& r) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r.w[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
 }
 
 // Codes of the 8-bit moments: the top bits of the fp32 magnitude, its exponent
 // counted from a power of two that the block's largest finite magnitude sets.
-// rnd16 enters at the top of the dropped bits: the code is rounded up with the
-// probability of its distance to the lower code, so the stored moment is right
-// in the mean. Nearest rounding would hold v where it is: a step moves v by
-// (1 - b2) ~ 1e-3 of itself and the codes lie 1/8 to 1/4 apart.
+// u20 (16 random bits << 4) enters at the top of the dropped bits: the code is
+// rounded up with the probability of its distance to the lower code, so the
+// stored moment is right in the mean. Nearest rounding would hold v where it
+// is: a step moves v by (1 - b2) ~ 1e-3 of itself and the codes lie 1/8 to 1/4
+// apart.
 //   m: e4m3, largest magnitude in [2^7, 2^8) of the scale; below 2^-6 -> 0
 //   v: e5m2, largest in [2^14, 2^15); 0 < v below 2^-14 -> 2^-14, so no
 //      gradient is ever divided by a vanished v
-// Subnormal codes are not made. A value that is not finite has the NaN code.
-SVLA_DEV uint32_t encode_m(float x, uint32_t rnd16, uint32_t low) {
-  const uint32_t bits = __float_as_uint(x), mag = bits & 0x7fffffffu;
-  const int code = (int)((mag + (rnd16 << 4)) >> 20) - (int)low;
-  const uint32_t c = code < 8 ? 0u : (uint32_t)code | ((bits >> 24) & 0x80u);
-  return mag >= 0x7f800000u ? 0x7fu : c;
+// Subnormal codes are not made. Values that are not finite are put in later.
+SVLA_DEV uint32_t encode_m(float x, uint32_t u20, uint32_t low) {
+  const uint32_t bits = __float_as_uint(x);
+  const int code = (int)(((bits & 0x7fffffffu) + u20) >> 20) - (int)low;
+  return code < 8 ? 0u : (uint32_t)code | ((bits >> 24) & 0x80u);
 }
-SVLA_DEV uint32_t encode_v(float x, uint32_t rnd16, uint32_t low) {
+SVLA_DEV uint32_t encode_v(float x, uint32_t u20, uint32_t low) {
   const uint32_t mag = __float_as_uint(x);
-  const int code = (int)((mag + (rnd16 << 5)) >> 21) - (int)low;
-  const uint32_t c = mag == 0 ? 0u : (uint32_t)max(code, 4);
-  return mag >= 0x7f800000u ? 0x7fu : c;
+  const int code = max((int)(((mag >> 1) + u20) >> 20) - (int)low, 4);
+  return mag == 0 ? 0u : (uint32_t)code;
 }
-SVLA_DEV uint32_t finite_mag(float x) {
-  const uint32_t mag = __float_as_uint(x) & 0x7fffffffu;
-  return mag >= 0x7f800000u ? 0u : mag;
-}
+SVLA_DEV uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+constexpr uint32_t INF_MAG = 0x7f800000u;
 
-// one element, both moments in fp32
+// One element: the moments, each product and sum rounded to fp32 by itself, and
+// the parameter.
 SVLA_DEV void update1(const AdamwCoefs& c, float keep, float g, float& p, float& m, float& v) {
   m = __fadd_rn(__fmul_rn(m, c.b1), __fmul_rn(g, c.c1));
   v = __fadd_rn(__fmul_rn(v, c.b2), __fmul_rn(__fmul_rn(g, g), c.c2));
-  const float denom = __fadd_rn(__fmul_rn(__fsqrt_rn(v), c.isb2), c.eps);
-  p = __fsub_rn(__fmul_rn(p, keep), __fmul_rn(__fdiv_rn(m, denom), c.step_size));
+  const float q = __fdiv_rn(m, __fmaf_rn(__fsqrt_rn(v), c.isb2, c.eps));
+  p = __fmaf_rn(-q, c.step_size, p * keep);
+}
+
+// The 8-bit step of a warp's block whatever its values: a zero v, moments near
+// the ends of fp32's range, or ones that are not finite (they take the NaN
+// code; the scales are those of the finite ones).
+template <typename TP, typename TG>
+SVLA_DEV void general8(const AdamwCoefs& c, float keep, float clip, const TP* pp, const TG* gp, const uint8_t* mp,
+                       const uint8_t* vp, bool vec, int left, int lane, float ms, float vs, const uint32_t (&r)[4],
+                       float (&p)[8], Raw8<uint8_t>& rm, Raw8<uint8_t>& rv, uint32_t& mx, uint32_t& vx) {
+  Raw8<TP> rp;
+  Raw8<TG> rg;
+  raw_load(pp, vec, left, lane, rp);
+  raw_load(gp, vec, left, lane, rg);
+  raw_load(mp, vec, left, lane, rm);
+  raw_load(vp, vec, left, lane, rv);
+  float m[8], v[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 x = decode_m2((rm.w[k >> 1] >> (16 * (k & 1))) & 0xffffu);
+    const float2 y = k & 1 ? decode_v2<1>(rv.w[k >> 1]) : decode_v2<0>(rv.w[k >> 1]);
+    m[2 * k] = __fmul_rn(x.x, ms), m[2 * k + 1] = __fmul_rn(x.y, ms);
+    v[2 * k] = __fmul_rn(y.x, vs), v[2 * k + 1] = __fmul_rn(y.y, vs);
+  }
+  mx = vx = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    p[j] = value(rp, j);
+    update1(c, keep, __fmul_rn(value(rg, j), clip), p[j], m[j], v[j]);
+    if (magnitude(m[j]) < INF_MAG) mx = max(mx, magnitude(m[j]));
+    if (magnitude(v[j]) < INF_MAG) vx = max(vx, magnitude(v[j]));
+  }
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  vx = __reduce_max_sync(0xffffffffu, vx);
+  const uint32_t em = (uint32_t)max((int)(mx >> 23) - 14, 0), ev = (uint32_t)max((int)(vx >> 23) - 29, 0);
+  uint32_t mc[8], vc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t u20 = (j & 1) ? (r[j >> 1] >> 12) & 0xffff0u : (r[j >> 1] & 0xffffu) << 4;
+    mc[j] = magnitude(m[j]) >= INF_MAG ? 0x7fu : encode_m(m[j], u20, em << 3);
+    vc[j] = magnitude(v[j]) >= INF_MAG ? 0x7fu : encode_v(v[j], u20, ev << 2);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    rm.w[k] = mc[4 * k] | mc[4 * k + 1] << 8 | mc[4 * k + 2] << 16 | mc[4 * k + 3] << 24;
+    rv.w[k] = vc[4 * k] | vc[4 * k + 1] << 8 | vc[4 * k + 2] << 16 | vc[4 * k + 3] << 24;
+  }
+}
+
+// The usual case of the 8-bit step: v below 2^100 (its product with 2^24 is
+// finite), |m| below 2^13 (the factor 2^-120 / m_scale is a normal number).
+constexpr uint32_t VX_USUAL = (127u + 100u) << 23, MX_USUAL = (127u + 13u) << 23;
+SVLA_DEV float sqrt_approx(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+SVLA_DEV float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // ---------------------------------------------------------------------------
@@ -145,17 +334,11 @@ __global__ void __launch_bounds__(ADAMW_THREADS) grad_norm_kernel(const __grid_c
     while (blk >= tab.first[t + 1]) ++t;
     const AdamwEntry& e = tab.e[t];
     const long long base = (long long)(blk - tab.first[t]) * ADAMW_BLOCK;
-    const TG* g = reinterpret_cast<const TG*>(e.g) + base;
-    const long long left = e.n - base;
-    float x[8];
-    if ((tab.flags[t] & AF_VEC) && left >= ADAMW_BLOCK) {
-      load8(g + lane * 8, x);
-    } else {
+    const int left = (int)min(e.n - base, (long long)ADAMW_BLOCK);
+    Raw8<TG> r;
+    raw_load(reinterpret_cast<const TG*>(e.g) + base, (tab.flags[t] & AF_VEC) && left == ADAMW_BLOCK, left, lane, r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = j * 32 + lane < left ? load1(g + j * 32 + lane) : 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j & 1] = fma((double)x[j], (double)x[j], acc[j & 1]);
+    for (int j = 0; j < 8; ++j) acc[j & 1] = fma((double)value(r, j), (double)value(r, j), acc[j & 1]);
   }
   double s = acc[0] + acc[1];
 #pragma unroll
@@ -175,14 +358,19 @@ __global__ void __launch_bounds__(ADAMW_THREADS) grad_norm_kernel(const __grid_c
 // are walked from its end, where the norm's pass over the gradients has just
 // been: the part of them that L2 still holds is not read from memory again.
 // ---------------------------------------------------------------------------
+#ifndef MINB32
+#define MINB32 3
+#define MINB8 3
+#endif
 template <typename TP, typename TG, int BITS>
-__global__ void __launch_bounds__(ADAMW_THREADS) adamw_kernel(const __grid_constant__ AdamwTable tab,
+__global__ void __launch_bounds__(ADAMW_THREADS, BITS == 32 ? MINB32 : MINB8) adamw_kernel(const __grid_constant__ AdamwTable tab,
                                                               const __grid_constant__ AdamwCoefs c0,
                                                               const double* __restrict__ partial, int n_partial,
                                                               float* __restrict__ grad_norm) {
   __shared__ double part[ADAMW_WARPS];
   __shared__ float s_clip;
   __shared__ float s_coef[3];
+  __shared__ __align__(16) uint16_t rnd[BITS == 8 ? ADAMW_WARPS : 1][ADAMW_BLOCK];
   // no early launch of dependents: what is written here may be a weight, which other kernels fetch before their wait
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -230,136 +418,120 @@ __global__ void __launch_bounds__(ADAMW_THREADS) adamw_kernel(const __grid_const
     const AdamwEntry& e = tab.e[t];
     const uint32_t tb = blk - tab.first[t];  // block of the tensor
     const long long base = (long long)tb * ADAMW_BLOCK;
-    const long long left = e.n - base;
-    const bool vec = (tab.flags[t] & AF_VEC) && left >= ADAMW_BLOCK;
+    const int left = (int)min(e.n - base, (long long)ADAMW_BLOCK);
+    const bool vec = (tab.flags[t] & AF_VEC) && left == ADAMW_BLOCK;
     const float keep = (tab.flags[t] & AF_DECAY) ? c.keep : 1.f;
     TP* pp = reinterpret_cast<TP*>(e.p) + base;
     const TG* gp = reinterpret_cast<const TG*>(e.g) + base;
-    uint16_t* cp = e.copy ? e.copy + base : nullptr;
-    float p[8], g[8], m[8], v[8];
-    // element of this lane's slot j: lane * 8 + j (vector accesses), else j * 32 + lane
-    if (vec) {
-      load8(pp + lane * 8, p);
-      load8(gp + lane * 8, g);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool in = j * 32 + lane < left;
-        p[j] = in ? load1(pp + j * 32 + lane) : 0.f;
-        g[j] = in ? load1(gp + j * 32 + lane) : 0.f;
-      }
-    }
+    Raw8<TP> rp;
+    Raw8<TG> rg;
+    raw_load(pp, vec, left, lane, rp);
+    raw_load(reinterpret_cast<const TG*>(e.g) + base, vec, left, lane, rg);
+    float p[8];
     if constexpr (BITS == 32) {
+      float m[8], v[8];
       float* mp = reinterpret_cast<float*>(e.m) + base;
       float* vp = reinterpret_cast<float*>(e.v) + base;
-      if (vec) {
-        load8(mp + lane * 8, m);
-        load8(vp + lane * 8, v);
-      } else {
+      Raw8<float> rm, rv;
+      raw_load(mp, vec, left, lane, rm);
+      raw_load(vp, vec, left, lane, rv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const bool in = j * 32 + lane < left;
-          m[j] = in ? mp[j * 32 + lane] : 0.f;
-          v[j] = in ? vp[j * 32 + lane] : 0.f;
-        }
+      for (int j = 0; j < 8; ++j) {
+        p[j] = value(rp, j);
+        m[j] = value(rm, j);
+        v[j] = value(rv, j);
+        update1(c, keep, __fmul_rn(value(rg, j), clip), p[j], m[j], v[j]);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) update1(c, keep, __fmul_rn(g[j], clip), p[j], m[j], v[j]);
-      if (vec) {
-        store8(mp + lane * 8, m);
-        store8(vp + lane * 8, v);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j * 32 + lane < left) {
-            mp[j * 32 + lane] = m[j];
-            vp[j * 32 + lane] = v[j];
-          }
-      }
+      pack(m, rm);
+      pack(v, rv);
+      raw_store(mp, vec, left, lane, rm);
+      raw_store(vp, vec, left, lane, rv);
     } else {
       uint8_t* mp = reinterpret_cast<uint8_t*>(e.m) + base;
       uint8_t* vp = reinterpret_cast<uint8_t*>(e.v) + base;
       const float ms = e.ms[tb], vs = e.vs[tb];
-      uint32_t mc[8], vc[8];
-      if (vec) {
-        const uint2 a = *reinterpret_cast<const uint2*>(mp + lane * 8);
-        const uint2 b = *reinterpret_cast<const uint2*>(vp + lane * 8);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 x = decode2<false>(((j < 2 ? a.x : a.y) >> (16 * (j & 1))) & 0xffffu);
-          const float2 y = decode2<true>(((j < 2 ? b.x : b.y) >> (16 * (j & 1))) & 0xffffu);
-          m[2 * j] = x.x, m[2 * j + 1] = x.y;
-          v[2 * j] = y.x, v[2 * j + 1] = y.y;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const bool in = j * 32 + lane < left;
-          m[j] = in ? decode2<false>(mp[j * 32 + lane]).x : 0.f;
-          v[j] = in ? decode2<true>(vp[j * 32 + lane]).x : 0.f;
-        }
-      }
-      uint32_t mx = 0, vx = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] = __fmul_rn(m[j], ms);
-        v[j] = __fmul_rn(v[j], vs);
-        update1(c, keep, __fmul_rn(g[j], clip), p[j], m[j], v[j]);
-        mx = max(mx, finite_mag(m[j]));
-        vx = max(vx, finite_mag(v[j]));
-      }
-      mx = __reduce_max_sync(0xffffffffu, mx);
-      vx = __reduce_max_sync(0xffffffffu, vx);
-      const uint32_t em = (uint32_t)max((int)(mx >> 23) - 14, 0), ev = (uint32_t)max((int)(vx >> 23) - 29, 0);
+      Raw8<uint8_t> rm, rv;
+      raw_load(mp, vec, left, lane, rm);
+      raw_load(vp, vec, left, lane, rv);
       // 16 random bits of element k: half k % 8 of the draw of its octet k / 8; both moments take the same bits
       // (each is right in the mean by itself, and the ratio's error is smaller when they round the same way)
       const unsigned long long oct = (unsigned long long)tb * 32 + lane;
       uint32_t r[4] = {(uint32_t)oct, (uint32_t)(oct >> 32), c.step, c.tensor0 + (uint32_t)t};
       philox4x32_10(r, c.k0, c.k1);
+      if (!vec) {  // to the lanes that hold the elements
+        __syncwarp();
+        *reinterpret_cast<uint4*>(&rnd[warp][lane * 8]) = make_uint4(r[0], r[1], r[2], r[3]);
+        __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t u;
-        if (vec) {
-          u = (r[j >> 1] >> (16 * (j & 1))) & 0xffffu;
-        } else {
-          const int src = j * 4 + (lane >> 3);
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = __shfl_sync(0xffffffffu, r[k], src);
-          const uint32_t a = (lane & 2) ? w[1] : w[0], b = (lane & 2) ? w[3] : w[2];
-          u = (((lane & 4) ? b : a) >> (16 * (lane & 1))) & 0xffffu;
-        }
-        mc[j] = encode_m(m[j], u, em << 3);
-        vc[j] = encode_v(v[j], u, ev << 2);
+        for (int k = 0; k < 4; ++k) r[k] = rnd[warp][2 * k * 32 + lane] | (uint32_t)rnd[warp][(2 * k + 1) * 32 + lane] << 16;
       }
-      if (vec) {
-        *reinterpret_cast<uint2*>(mp + lane * 8) =
-            make_uint2(mc[0] | mc[1] << 8 | mc[2] << 16 | mc[3] << 24, mc[4] | mc[5] << 8 | mc[6] << 16 | mc[7] << 24);
-        *reinterpret_cast<uint2*>(vp + lane * 8) =
-            make_uint2(vc[0] | vc[1] << 8 | vc[2] << 16 | vc[3] << 24, vc[4] | vc[5] << 8 | vc[6] << 16 | vc[7] << 24);
-      } else {
+      // the usual case, two elements at a time: no zero and no large v, all finite
+      const f32x2 z = both(c.minus0);
+      f32x2 m2[4], v2[4], p2[4], nan2 = both(0.f);
+      float mx = 0.f;
+      uint32_t vx = 0, vmin = 0xffffffffu;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j * 32 + lane < left) {
-            mp[j * 32 + lane] = (uint8_t)mc[j];
-            vp[j * 32 + lane] = (uint8_t)vc[j];
-          }
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = decode_m2((rm.w[k >> 1] >> (16 * (k & 1))) & 0xffffu);
+        const float2 y = k & 1 ? decode_v2<1>(rv.w[k >> 1]) : decode_v2<0>(rv.w[k >> 1]);
+        const f32x2 g2 = mul2(pair(value(rg, 2 * k), value(rg, 2 * k + 1)), both(clip));
+        m2[k] = add2(product2(mul2(pair(x.x, x.y), both(ms)), both(c.b1), z), product2(g2, both(c.c1), z));
+        v2[k] = add2(product2(mul2(pair(y.x, y.y), both(vs)), both(c.b2), z), product2(mul2(g2, g2), both(c.c2), z));
+        nan2 = fma2(m2[k], both(0.f), nan2);  // NaN if an m is not finite
+        const float2 mm = halves(m2[k]), vv = halves(v2[k]);
+        mx = fmaxf(mx, fmaxf(fabsf(mm.x), fabsf(mm.y)));
+        vx = max(vx, max(__float_as_uint(vv.x), __float_as_uint(vv.y)));
+        vmin = min(vmin, min(__float_as_uint(vv.x), __float_as_uint(vv.y)));
+        // v 2^24 is a normal number whatever v > 0, and finite: v < 2^100 here
+        const float2 s2 = halves(mul2(v2[k], both(16777216.f)));
+        const float2 root = make_float2(sqrt_approx(s2.x), sqrt_approx(s2.y));
+        const float2 den = halves(fma2(pair(root.x, root.y), both(c.isb2 * 0x1p-12f), both(c.eps)));
+        const f32x2 q = mul2(m2[k], pair(rcp_approx(den.x), rcp_approx(den.y)));
+        p2[k] = fma2(q, both(-c.step_size), mul2(pair(value(rp, 2 * k), value(rp, 2 * k + 1)), both(keep)));
+      }
+      const float2 nn = halves(nan2);
+      uint32_t mxb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+      vx = __reduce_max_sync(0xffffffffu, vx);
+      const bool odd = vmin == 0 || !(nn.x + nn.y == 0.f);
+      if (!__any_sync(0xffffffffu, odd) && vx < VX_USUAL && mxb < MX_USUAL) {
+        const uint32_t em = (uint32_t)max((int)(mxb >> 23) - 14, 0), ev = (uint32_t)max((int)(vx >> 23) - 29, 0);
+        // m / m_scale in two steps: the first takes the smallest normal code to 2^-126, so that what is below it is
+        // flushed to zero; the second back into the format's range (and -0 to 0)
+        const f32x2 down = both(__uint_as_float((127u + 127u - 120u - em - 7u) << 23)), up = both(0x1p120f);
+        const f32x2 vinv = both(__uint_as_float((254u - ev - 15u) << 23));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t u0 = (r[k] & 0xffffu) << 4, u1 = (r[k] >> 12) & 0xffff0u;
+          const float2 mm = halves(m2[k]), vv = halves(v2[k]);
+          const f32x2 mt = pair(__uint_as_float((__float_as_uint(mm.x) + u0) & 0xfff00000u),
+                                __uint_as_float((__float_as_uint(mm.y) + u1) & 0xfff00000u));
+          const f32x2 vt = pair(__uint_as_float((__float_as_uint(vv.x) + 2 * u0) & 0xffe00000u),
+                                __uint_as_float((__float_as_uint(vv.y) + 2 * u1) & 0xffe00000u));
+          const uint32_t mc = code_m2(fma2(mul2_ftz(mt, down), up, both(0.f)));
+          const float2 vy = halves(mul2(vt, vinv));
+          const uint32_t vc = code_v2(fmaxf(vy.x, 0x1p-14f), fmaxf(vy.y, 0x1p-14f));
+          rm.w[k >> 1] = k & 1 ? rm.w[k >> 1] | mc << 16 : mc;
+          rv.w[k >> 1] = k & 1 ? rv.w[k >> 1] | vc << 16 : vc;
+          const float2 pp2 = halves(p2[k]);
+          p[2 * k] = pp2.x;
+          p[2 * k + 1] = pp2.y;
+        }
+      } else {
+        general8(c, keep, clip, pp, gp, mp, vp, vec, left, lane, ms, vs, r, p, rm, rv, mxb, vx);
       }
       if (lane == 0) {
-        e.ms[tb] = mx ? __uint_as_float((em + 7) << 23) : 0.f;
-        e.vs[tb] = vx ? __uint_as_float((ev + 15) << 23) : 0.f;
+        e.ms[tb] = mxb ? __uint_as_float((uint32_t)(max((int)(mxb >> 23) - 14, 0) + 7) << 23) : 0.f;
+        e.vs[tb] = vx ? __uint_as_float((uint32_t)(max((int)(vx >> 23) - 29, 0) + 15) << 23) : 0.f;
       }
+      raw_store(mp, vec, left, lane, rm);
+      raw_store(vp, vec, left, lane, rv);
     }
-    if (vec) {
-      store8(pp + lane * 8, p);
-      if (cp) store8(cp + lane * 8, p);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j * 32 + lane < left) {
-          store1(pp + j * 32 + lane, p[j]);
-          if (cp) store1(cp + j * 32 + lane, p[j]);
-        }
+    pack(p, rp);
+    raw_store(pp, vec, left, lane, rp);
+    if (e.copy) {
+      Raw8<uint16_t> rc;
+      pack(p, rc);
+      raw_store(e.copy + base, vec, left, lane, rc);
     }
   }
   __threadfence();
@@ -473,6 +645,7 @@ svla_status adamw_checked(const svla_adamw_tensor* ts, int n, const svla_adamw_a
   c.b2 = (float)a->beta2;
   c.c2 = (float)(1.0 - a->beta2);
   c.eps = (float)a->eps;
+  c.minus0 = -0.f;
   c.max_norm = a->max_norm;
   c.k0 = (uint32_t)a->seed;
   c.k1 = (uint32_t)(a->seed >> 32);
@@ -511,8 +684,8 @@ svla_status adamw_checked(const svla_adamw_tensor* ts, int n, const svla_adamw_a
         const svla_adamw_tensor& t = ts[l * ADAMW_CAP + k];
         tab.e[k] = AdamwEntry{t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, reinterpret_cast<uint16_t*>(t.copy),
                               (long long)t.n};
-        const bool vec = (((uintptr_t)t.param | (uintptr_t)t.grad | (uintptr_t)t.copy) & 15) == 0 &&
-                         (((uintptr_t)t.m | (uintptr_t)t.v) & (a->state_bits == 32 ? 15 : 7)) == 0;
+        const bool vec = ((uintptr_t)t.param & (8 * pb - 1)) == 0 && ((uintptr_t)t.grad & (8 * gb - 1)) == 0 &&
+                         ((uintptr_t)t.copy & 15) == 0 && (((uintptr_t)t.m | (uintptr_t)t.v) & (8 * sb - 1)) == 0;
         tab.flags[k] = (uint8_t)((t.decay ? AF_DECAY : 0) | (vec ? AF_VEC : 0));
         tab.first[k] = (uint32_t)nb;
         nb += (unsigned long long)((t.n + ADAMW_BLOCK - 1) / ADAMW_BLOCK);

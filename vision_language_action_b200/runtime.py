@@ -458,8 +458,8 @@ class AdamW:
         self.device, self.state_bits, self.lr, self.steps = dev, state_bits, lr, int(step)
         size = [p.numel() for p in self.params]
         if state is None:
-            # one buffer a moment; every tensor's part starts on 16 bytes
-            unit = 4 if state_bits == 32 else 16
+            # one buffer a moment; every tensor's part starts at a multiple of 8 elements
+            unit = 8
             at = [0]
             for k in size:
                 at.append(at[-1] + (k + unit - 1) // unit * unit)
