@@ -16,10 +16,14 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <cstring>
 #include <exception>
+#include <memory>
 #include <string>
+#include <type_traits>
 #include <utility>
 #include <vector>
 
@@ -33,9 +37,13 @@ namespace svla {
 namespace {
 
 constexpr int ADAMW_BLOCK = 256;   // elements of a warp's task = elements that share a scale
-constexpr int ADAMW_CAP = 400;     // tensors of one launch (27.6 KB of the 32,764 bytes of kernel parameters)
+constexpr int ADAMW_CAP = 400;     // tensors of one launch (28.1 KB of the 32,764 bytes of kernel parameters)
+constexpr int ADAMW_FEW = 32;      // of a launch of a short list: the parameters are copied at every launch
+constexpr int ADAMW_HINTS = 256;   // spans of chunks whose first tensor the table names
 constexpr int ADAMW_THREADS = 256;
 constexpr int ADAMW_WARPS = ADAMW_THREADS / 32;
+constexpr int ADAMW_CHUNK = ADAMW_WARPS * ADAMW_BLOCK;  // elements of a block's task, of one tensor
+constexpr int NORM_THREADS = 512;
 constexpr int NORM_BLOCKS = 592;   // blocks (and partial sums) of one launch of the norm: 4 on each of 148 SMs
 
 struct AdamwEntry {
@@ -49,34 +57,40 @@ struct AdamwEntry {
   long long n;
 };
 
+template <int CAP>
 struct AdamwTable {
-  AdamwEntry e[ADAMW_CAP];
-  uint32_t first[ADAMW_CAP + 1];  // first 256-element block of each tensor; first[count] = all blocks
-  uint8_t flags[ADAMW_CAP];       // 1: weight decay, 2: every pointer allows the vector accesses
-  int count;
+  AdamwEntry e[CAP];
+  uint32_t first[CAP + 1];  // first chunk of each tensor; first[count] = all chunks
+  uint16_t hint[ADAMW_HINTS + 1]; // tensor of chunk k << shift (the last one for chunks past the end)
+  uint8_t flags[CAP];             // 1: weight decay, 2: every pointer allows the vector accesses
+  int count, shift;
 };
 constexpr uint8_t AF_DECAY = 1, AF_VEC = 2;
 
 struct AdamwCoefs {
+  // pairs of equal values, operands of the packed arithmetic straight from the constant bank
+  unsigned long long b1_2, c1_2, b2_2, c2_2, eps_2, minus0_2, two24_2;
+  uint32_t key[20];  // Philox round keys
   float b1, c1, b2, c2, eps;
   float keep;       // 1 - lr wd
   float step_size;  // lr / (1 - b1^t)
   float isb2;       // 1 / sqrt(1 - b2^t)
-  float minus0;     // -0 (product2)
   double max_norm;  // 0: no clip
-  uint32_t k0, k1, step, tensor0;
+  uint32_t step, tensor0;
   // read on the device instead of the host's numbers, where given
   const long long* step_dev;
   const double* lr_dev;
   double lr, beta1, beta2, wd;
 };
 
-// tensor of block `blk`: the last t with first[t] <= blk (empty tensors have no block)
-SVLA_DEV int find_tensor(const AdamwTable& t, uint32_t blk) {
-  int lo = 0, hi = t.count - 1;
+// tensor of a chunk: the last t with first[t] <= chunk (empty tensors have none),
+// searched between the tensors of its span's ends
+template <int CAP>
+SVLA_DEV int find_tensor(const AdamwTable<CAP>& t, uint32_t chunk) {
+  int lo = t.hint[chunk >> t.shift], hi = t.hint[(chunk >> t.shift) + 1];
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (t.first[mid] <= blk)
+    if (t.first[mid] <= chunk)
       lo = mid;
     else
       hi = mid - 1;
@@ -136,41 +150,67 @@ SVLA_DEV float2 decode_v2(uint32_t four) {
   const uint32_t h = __byte_perm(four, 0, K ? 0x3424 : 0x1404);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-// two values that the formats hold -> their codes (lo in the low byte)
-SVLA_DEV uint32_t code_m2(f32x2 x) {
-  uint16_t r;
+// Two values -> fp16, the mantissa cut off (lo in the low half).
+SVLA_DEV uint32_t cut_f16x2(f32x2 x) {
+  uint32_t r;
   const float2 f = halves(x);
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(f.y), "f"(f.x));
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
   return r;
 }
-SVLA_DEV uint32_t code_v2(float lo, float hi) {
+// Codes of two moments that are divided by their scale, with the random bits
+// added below what the code keeps.
+//   m, further divided by 2^8: cut to 3 mantissa bits; what is below 2^-6 of the
+//   scale is a subnormal fp16 number here, and the product with 2^8 flushes it
+//   (and makes a -0 0).
+//   v: an e5m2 code is the upper byte of an fp16 number, at least 2^-14 here.
+SVLA_DEV uint32_t code_m2(f32x2 x) {
+  uint32_t h;
   uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  asm("fma.rn.ftz.f16x2 %0, %1, %2, %3;" : "=r"(h) : "r"(cut_f16x2(x) & 0xff80ff80u), "r"(0x5c005c00u), "r"(0u));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+SVLA_DEV uint32_t half_v2(f32x2 x) {
+  uint32_t h;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(h) : "r"(cut_f16x2(x)), "r"(0x04000400u));
+  return h;
+}
+// the larger (smaller) of three, NaN if one is NaN
+SVLA_DEV float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+SVLA_DEV float min3(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
-// 8 elements of this lane from a warp's 256, raw, packed into words. `vec`: the
-// consecutive elements lane * 8 .., one 32-byte (fp32), 16-byte (bf16) or 8-byte
+// 8 elements of this lane from its warp's 256 of a chunk, raw, packed into words.
+// `vec`: the consecutive elements from `at`, one 32-byte (fp32), 16-byte (bf16) or 8-byte
 // (codes) access; else (a tensor's last, shorter block, or a tensor at an odd
-// address) the elements lane, lane + 32, .., zeros past the tensor's end.
+// address) every 32nd element of the warp's, of which `left` exist; zeros past them.
 template <typename E>
 struct Raw8 {
   uint32_t w[2 * sizeof(E)];
 };
 template <typename E>
-SVLA_DEV void raw_load(const E* p, bool vec, int left, int lane, Raw8<E>& r) {
+SVLA_DEV void raw_load(const E* p, bool vec, int left, int at, Raw8<E>& r) {
   if (vec) {
     if constexpr (sizeof(E) == 4) {
-      ld_global_v8(p + lane * 8, r.w);
+      ld_global_v8(p + at, r.w);
     } else if constexpr (sizeof(E) == 2) {
-      const uint4 q = *reinterpret_cast<const uint4*>(p + lane * 8);
+      const uint4 q = *reinterpret_cast<const uint4*>(p + at);
       r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
     } else {
-      const uint2 q = *reinterpret_cast<const uint2*>(p + lane * 8);
+      const uint2 q = *reinterpret_cast<const uint2*>(p + at);
       r.w[0] = q.x, r.w[1] = q.y;
     }
     return;
   }
+  const int lane = (at >> 3) & 31;
+  p += at - lane * 8;
   uint32_t x[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -188,17 +228,19 @@ SVLA_DEV void raw_load(const E* p, bool vec, int left, int lane, Raw8<E>& r) {
   }
 }
 template <typename E>
-SVLA_DEV void raw_store(E* p, bool vec, int left, int lane, const Raw8<E>& r) {
+SVLA_DEV void raw_store(E* p, bool vec, int left, int at, const Raw8<E>& r) {
   if (vec) {
     if constexpr (sizeof(E) == 4)
-      st_global_v8(p + lane * 8, r.w);
+      st_global_v8(p + at, r.w);
     else if constexpr (sizeof(E) == 2)
-      *reinterpret_cast<uint4*>(p + lane * 8) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+      *reinterpret_cast<uint4*>(p + at) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
     else
-      *reinterpret_cast<uint2*>(p + lane * 8) = make_uint2(r.w[0], r.w[1]);
+      *reinterpret_cast<uint2*>(p + at) = make_uint2(r.w[0], r.w[1]);
     return;
   }
   constexpr int PER = 4 / sizeof(E);
+  const int lane = (at >> 3) & 31;
+  p += at - lane * 8;
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     if (j * 32 + lane < left) {
@@ -248,45 +290,96 @@ constexpr uint32_t INF_MAG = 0x7f800000u;
 
 // One element: the moments, each product and sum rounded to fp32 by itself, and
 // the parameter.
-SVLA_DEV void update1(const AdamwCoefs& c, float keep, float g, float& p, float& m, float& v) {
+SVLA_DEV void update1(const AdamwCoefs& c, float keep, float isb2, float step_size, float g, float& p, float& m, float& v) {
   m = __fadd_rn(__fmul_rn(m, c.b1), __fmul_rn(g, c.c1));
   v = __fadd_rn(__fmul_rn(v, c.b2), __fmul_rn(__fmul_rn(g, g), c.c2));
-  const float q = __fdiv_rn(m, __fmaf_rn(__fsqrt_rn(v), c.isb2, c.eps));
-  p = __fmaf_rn(-q, c.step_size, p * keep);
+  const float q = __fdiv_rn(m, __fmaf_rn(__fsqrt_rn(v), isb2, c.eps));
+  p = __fmaf_rn(-q, step_size, p * keep);
 }
+
+// Where a warp's 256 elements lie: the arrays from the chunk's first element, the
+// block's scales, and what all of its elements share.
+template <typename TP, typename TG, typename TS>
+struct Place {
+  TP* p;
+  const TG* g;
+  TS *m, *v;
+  uint16_t* copy;
+  float *ms, *vs;
+  int left, at;  // elements of this warp; this lane's first one of the chunk (vector accesses)
+  bool vec;      // all there, and the tensor's pointers allow the wide accesses
+  float keep, clip, isb2, step_size;
+};
+template <typename TP, typename TG, typename TS>
+struct Loaded {
+  Raw8<TP> p;
+  Raw8<TG> g;
+  Raw8<TS> m, v;
+  SVLA_DEV void load(const Place<TP, TG, TS>& a) {
+    if (a.vec) {
+      raw_load(a.p, true, 0, a.at, p);
+      raw_load(a.g, true, 0, a.at, g);
+      raw_load(a.m, true, 0, a.at, m);
+      raw_load(a.v, true, 0, a.at, v);
+    } else {
+      raw_load(a.p, false, a.left, a.at, p);
+      raw_load(a.g, false, a.left, a.at, g);
+      raw_load(a.m, false, a.left, a.at, m);
+      raw_load(a.v, false, a.left, a.at, v);
+    }
+  }
+};
+template <typename TP, typename TG, typename TS>
+SVLA_DEV void store_all(const Place<TP, TG, TS>& a, const float (&p)[8], const Raw8<TS>& m, const Raw8<TS>& v) {
+  Raw8<TP> rp;
+  Raw8<uint16_t> rc;
+  pack(p, rp);
+  pack(p, rc);
+  if (a.vec) {
+    raw_store(a.m, true, 0, a.at, m);
+    raw_store(a.v, true, 0, a.at, v);
+    raw_store(a.p, true, 0, a.at, rp);
+    if (a.copy) raw_store(a.copy, true, 0, a.at, rc);
+  } else {
+    raw_store(a.m, false, a.left, a.at, m);
+    raw_store(a.v, false, a.left, a.at, v);
+    raw_store(a.p, false, a.left, a.at, rp);
+    if (a.copy) raw_store(a.copy, false, a.left, a.at, rc);
+  }
+}
+// fields of the block scales from the largest magnitudes' bits
+SVLA_DEV uint32_t m_field(uint32_t mx) { return (uint32_t)max((int)(mx >> 23) - 14, 0); }
+SVLA_DEV uint32_t v_field(uint32_t vx) { return (uint32_t)max((int)(vx >> 23) - 29, 0); }
 
 // The 8-bit step of a warp's block whatever its values: a zero v, moments near
 // the ends of fp32's range, or ones that are not finite (they take the NaN
-// code; the scales are those of the finite ones).
+// code; the scales are those of the finite ones). Not inlined: its registers
+// are not the usual case's.
 template <typename TP, typename TG>
-SVLA_DEV void general8(const AdamwCoefs& c, float keep, float clip, const TP* pp, const TG* gp, const uint8_t* mp,
-                       const uint8_t* vp, bool vec, int left, int lane, float ms, float vs, const uint32_t (&r)[4],
-                       float (&p)[8], Raw8<uint8_t>& rm, Raw8<uint8_t>& rv, uint32_t& mx, uint32_t& vx) {
-  Raw8<TP> rp;
-  Raw8<TG> rg;
-  raw_load(pp, vec, left, lane, rp);
-  raw_load(gp, vec, left, lane, rg);
-  raw_load(mp, vec, left, lane, rm);
-  raw_load(vp, vec, left, lane, rv);
-  float m[8], v[8];
+__device__ __noinline__ void general8(const AdamwCoefs& c, const Place<TP, TG, uint8_t> a, uint4 rnd4) {
+  const uint32_t r[4] = {rnd4.x, rnd4.y, rnd4.z, rnd4.w};
+  Loaded<TP, TG, uint8_t> in;
+  in.load(a);
+  const float ms = *a.ms, vs = *a.vs;
+  float p[8], m[8], v[8];
+  uint32_t mx = 0, vx = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float2 x = decode_m2((rm.w[k >> 1] >> (16 * (k & 1))) & 0xffffu);
-    const float2 y = k & 1 ? decode_v2<1>(rv.w[k >> 1]) : decode_v2<0>(rv.w[k >> 1]);
+    const float2 x = decode_m2((in.m.w[k >> 1] >> (16 * (k & 1))) & 0xffffu);
+    const float2 y = k & 1 ? decode_v2<1>(in.v.w[k >> 1]) : decode_v2<0>(in.v.w[k >> 1]);
     m[2 * k] = __fmul_rn(x.x, ms), m[2 * k + 1] = __fmul_rn(x.y, ms);
     v[2 * k] = __fmul_rn(y.x, vs), v[2 * k + 1] = __fmul_rn(y.y, vs);
   }
-  mx = vx = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    p[j] = value(rp, j);
-    update1(c, keep, __fmul_rn(value(rg, j), clip), p[j], m[j], v[j]);
+    p[j] = value(in.p, j);
+    update1(c, a.keep, a.isb2, a.step_size, __fmul_rn(value(in.g, j), a.clip), p[j], m[j], v[j]);
     if (magnitude(m[j]) < INF_MAG) mx = max(mx, magnitude(m[j]));
     if (magnitude(v[j]) < INF_MAG) vx = max(vx, magnitude(v[j]));
   }
   mx = __reduce_max_sync(0xffffffffu, mx);
   vx = __reduce_max_sync(0xffffffffu, vx);
-  const uint32_t em = (uint32_t)max((int)(mx >> 23) - 14, 0), ev = (uint32_t)max((int)(vx >> 23) - 29, 0);
+  const uint32_t em = m_field(mx), ev = v_field(vx);
   uint32_t mc[8], vc[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -296,14 +389,19 @@ SVLA_DEV void general8(const AdamwCoefs& c, float keep, float clip, const TP* pp
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    rm.w[k] = mc[4 * k] | mc[4 * k + 1] << 8 | mc[4 * k + 2] << 16 | mc[4 * k + 3] << 24;
-    rv.w[k] = vc[4 * k] | vc[4 * k + 1] << 8 | vc[4 * k + 2] << 16 | vc[4 * k + 3] << 24;
+    in.m.w[k] = mc[4 * k] | mc[4 * k + 1] << 8 | mc[4 * k + 2] << 16 | mc[4 * k + 3] << 24;
+    in.v.w[k] = vc[4 * k] | vc[4 * k + 1] << 8 | vc[4 * k + 2] << 16 | vc[4 * k + 3] << 24;
+  }
+  store_all(a, p, in.m, in.v);
+  __syncwarp();  // every lane has read the scales
+  if ((threadIdx.x & 31) == 0) {
+    *a.ms = mx ? __uint_as_float((em + 7) << 23) : 0.f;
+    *a.vs = vx ? __uint_as_float((ev + 15) << 23) : 0.f;
   }
 }
 
-// The usual case of the 8-bit step: v below 2^100 (its product with 2^24 is
-// finite), |m| below 2^13 (the factor 2^-120 / m_scale is a normal number).
-constexpr uint32_t VX_USUAL = (127u + 100u) << 23, MX_USUAL = (127u + 13u) << 23;
+// The usual case of the 8-bit step has v below 2^100 (its product with 2^24 is finite).
+constexpr uint32_t VX_USUAL = (127u + 100u) << 23;
 SVLA_DEV float sqrt_approx(float x) {
   float r;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -320,23 +418,24 @@ SVLA_DEV float rcp_approx(float x) {
 // the clip factor's fp32 rounding) does not depend on the order of the sum in
 // practice; fixed order all the same. partial[blockIdx.x] of this launch.
 // ---------------------------------------------------------------------------
-template <typename TG>
-__global__ void __launch_bounds__(ADAMW_THREADS) grad_norm_kernel(const __grid_constant__ AdamwTable tab,
-                                                                  double* __restrict__ partial) {
-  __shared__ double part[ADAMW_WARPS];
+template <typename TG, int CAP>
+__global__ void __launch_bounds__(NORM_THREADS) grad_norm_kernel(const __grid_constant__ AdamwTable<CAP> tab,
+                                                                 double* __restrict__ partial) {
+  __shared__ double part[NORM_THREADS / 32];
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t nb = tab.first[tab.count], stride = gridDim.x * ADAMW_WARPS;
+  const int wc = warp % ADAMW_WARPS;  // place in the chunk: the block takes NORM_THREADS / ADAMW_THREADS chunks at a time
+  const uint32_t chunks = tab.first[tab.count], stride = gridDim.x * (NORM_THREADS / ADAMW_THREADS);
   double acc[2] = {0.0, 0.0};
-  uint32_t blk = blockIdx.x * ADAMW_WARPS + warp;
-  int t = blk < nb ? find_tensor(tab, blk) : 0;
-  for (; blk < nb; blk += stride) {
-    while (blk >= tab.first[t + 1]) ++t;
+#pragma unroll 2
+  for (uint32_t chunk = blockIdx.x * (NORM_THREADS / ADAMW_THREADS) + warp / ADAMW_WARPS; chunk < chunks; chunk += stride) {
+    const int t = find_tensor(tab, chunk);
     const AdamwEntry& e = tab.e[t];
-    const long long base = (long long)(blk - tab.first[t]) * ADAMW_BLOCK;
-    const int left = (int)min(e.n - base, (long long)ADAMW_BLOCK);
+    const long long base = (long long)(chunk - tab.first[t]) * ADAMW_CHUNK;
+    const int left = (int)min(e.n - base, (long long)ADAMW_CHUNK) - wc * ADAMW_BLOCK;
     Raw8<TG> r;
-    raw_load(reinterpret_cast<const TG*>(e.g) + base, (tab.flags[t] & AF_VEC) && left == ADAMW_BLOCK, left, lane, r);
+    raw_load(reinterpret_cast<const TG*>(e.g) + base, (tab.flags[t] & AF_VEC) && left >= ADAMW_BLOCK, left,
+             wc * ADAMW_BLOCK + lane * 8, r);
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j & 1] = fma((double)value(r, j), (double)value(r, j), acc[j & 1]);
   }
@@ -347,8 +446,103 @@ __global__ void __launch_bounds__(ADAMW_THREADS) grad_norm_kernel(const __grid_c
   __syncthreads();
   if (threadIdx.x == 0) {
     double all = 0.0;
-    for (int w = 0; w < ADAMW_WARPS; ++w) all += part[w];
+    for (int w = 0; w < NORM_THREADS / 32; ++w) all += part[w];
     partial[blockIdx.x] = all;
+  }
+}
+
+template <typename TP, typename TG>
+SVLA_DEV void update32(const AdamwCoefs& c, const Place<TP, TG, float>& a) {
+  Loaded<TP, TG, float> in;
+  in.load(a);
+  float p[8], m[8], v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    p[j] = value(in.p, j);
+    m[j] = value(in.m, j);
+    v[j] = value(in.v, j);
+    update1(c, a.keep, a.isb2, a.step_size, __fmul_rn(value(in.g, j), a.clip), p[j], m[j], v[j]);
+  }
+  pack(m, in.m);
+  pack(v, in.v);
+  store_all(a, p, in.m, in.v);
+}
+
+// The usual case in packed pairs: every v positive and below 2^100, all finite.
+// Else the block is done by general8.
+template <typename TP, typename TG>
+SVLA_DEV void update8(const AdamwCoefs& c, const Place<TP, TG, uint8_t>& a, uint32_t block, uint32_t step, uint32_t tensor,
+                      int lane, uint16_t* rnd) {
+  Loaded<TP, TG, uint8_t> in;
+  in.load(a);
+  const float ms = *a.ms, vs = *a.vs;
+  // 16 random bits of element k: half k % 8 of the draw of its octet k / 8; both moments take the same bits
+  // (each is right in the mean by itself, and the ratio's error is smaller when they round the same way)
+  const unsigned long long oct = (unsigned long long)block * 32 + lane;
+  uint32_t r[4] = {(uint32_t)oct, (uint32_t)(oct >> 32), step, tensor};
+#pragma unroll
+  for (int k = 0; k < 10; ++k) philox_round(r, c.key[2 * k], c.key[2 * k + 1]);
+  if (!a.vec) {  // to the lanes that hold the elements
+    __syncwarp();
+    *reinterpret_cast<uint4*>(&rnd[lane * 8]) = make_uint4(r[0], r[1], r[2], r[3]);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = rnd[2 * k * 32 + lane] | (uint32_t)rnd[(2 * k + 1) * 32 + lane] << 16;
+  }
+  const f32x2 z = c.minus0_2;
+  f32x2 m2[4], v2[4];
+  float mx = 0.f, vx = 0.f, vmin = INFINITY;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 x = decode_m2((in.m.w[k >> 1] >> (16 * (k & 1))) & 0xffffu);
+    const float2 y = k & 1 ? decode_v2<1>(in.v.w[k >> 1]) : decode_v2<0>(in.v.w[k >> 1]);
+    const f32x2 g2 = mul2(pair(value(in.g, 2 * k), value(in.g, 2 * k + 1)), both(a.clip));
+    m2[k] = add2(product2(mul2(pair(x.x, x.y), both(ms)), c.b1_2, z), product2(g2, c.c1_2, z));
+    v2[k] = add2(product2(mul2(pair(y.x, y.y), both(vs)), c.b2_2, z), product2(mul2(g2, g2), c.c2_2, z));
+    const float2 mm = halves(m2[k]), vv = halves(v2[k]);
+    mx = max3_abs(mx, mm.x, mm.y);
+    vx = max3_abs(vx, vv.x, vv.y);
+    vmin = min3(vmin, vv.x, vv.y);
+  }
+  const uint32_t mxb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+  const uint32_t vxb = __reduce_max_sync(0xffffffffu, __float_as_uint(vx));
+  if (!__all_sync(0xffffffffu, vmin > 0.f && mxb < INF_MAG && vxb < VX_USUAL)) {
+    general8(c, a, make_uint4(r[0], r[1], r[2], r[3]));
+    return;
+  }
+  float p[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    // v 2^24 is a normal number whatever v > 0, and finite: v < 2^100 here
+    const float2 s2 = halves(mul2(v2[k], c.two24_2));
+    const float2 root = make_float2(sqrt_approx(s2.x), sqrt_approx(s2.y));
+    const float2 den = halves(fma2(pair(root.x, root.y), both(a.isb2 * 0x1p-12f), c.eps_2));
+    const f32x2 q = mul2(m2[k], pair(rcp_approx(den.x), rcp_approx(den.y)));
+    const float2 pn = halves(fma2(q, both(-a.step_size), mul2(pair(value(in.p, 2 * k), value(in.p, 2 * k + 1)), both(a.keep))));
+    p[2 * k] = pn.x;
+    p[2 * k + 1] = pn.y;
+  }
+  const uint32_t em = m_field(mxb), ev = v_field(vxb);
+  const f32x2 minv = both(__uint_as_float((254u - 7u - 8u - em) << 23));  // 2^-8 / scale of m
+  const f32x2 vinv = both(__uint_as_float((254u - 15u - ev) << 23));
+  uint32_t vh[4], mc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t u0 = r[k] & 0xffffu, u1 = r[k] >> 16;
+    const float2 mm = halves(m2[k]), vv = halves(v2[k]);
+    mc[k] = code_m2(mul2(pair(__uint_as_float(__float_as_uint(mm.x) + u0 * 16u),
+                              __uint_as_float(__float_as_uint(mm.y) + u1 * 16u)), minv));
+    vh[k] = half_v2(mul2(pair(__uint_as_float(__float_as_uint(vv.x) + u0 * 32u),
+                              __uint_as_float(__float_as_uint(vv.y) + u1 * 32u)), vinv));
+  }
+  in.m.w[0] = __byte_perm(mc[0], mc[1], 0x5410);
+  in.m.w[1] = __byte_perm(mc[2], mc[3], 0x5410);
+  in.v.w[0] = __byte_perm(vh[0], vh[1], 0x7531);
+  in.v.w[1] = __byte_perm(vh[2], vh[3], 0x7531);
+  store_all(a, p, in.m, in.v);
+  if (lane == 0) {
+    *a.ms = mxb ? __uint_as_float((em + 7) << 23) : 0.f;
+    *a.vs = __uint_as_float((ev + 15) << 23);
   }
 }
 
@@ -358,15 +552,12 @@ __global__ void __launch_bounds__(ADAMW_THREADS) grad_norm_kernel(const __grid_c
 // are walked from its end, where the norm's pass over the gradients has just
 // been: the part of them that L2 still holds is not read from memory again.
 // ---------------------------------------------------------------------------
-#ifndef MINB32
-#define MINB32 3
-#define MINB8 3
-#endif
-template <typename TP, typename TG, int BITS>
-__global__ void __launch_bounds__(ADAMW_THREADS, BITS == 32 ? MINB32 : MINB8) adamw_kernel(const __grid_constant__ AdamwTable tab,
-                                                              const __grid_constant__ AdamwCoefs c0,
+template <typename TP, typename TG, int BITS, int CAP>
+__global__ void __launch_bounds__(ADAMW_THREADS, BITS == 8 && sizeof(TP) == 2 ? 4 : 3) adamw_kernel(const __grid_constant__ AdamwTable<CAP> tab,
+                                                              const __grid_constant__ AdamwCoefs c,
                                                               const double* __restrict__ partial, int n_partial,
                                                               float* __restrict__ grad_norm) {
+  typedef typename std::conditional<BITS == 32, float, uint8_t>::type TS;
   __shared__ double part[ADAMW_WARPS];
   __shared__ float s_clip;
   __shared__ float s_coef[3];
@@ -374,8 +565,8 @@ __global__ void __launch_bounds__(ADAMW_THREADS, BITS == 32 ? MINB32 : MINB8) ad
   // no early launch of dependents: what is written here may be a weight, which other kernels fetch before their wait
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  AdamwCoefs c = c0;
-  float clip = 1.f;
+  float clip = 1.f, keep_all = c.keep, step_size = c.step_size, isb2 = c.isb2;
+  uint32_t step = c.step;
   if (c.step_dev || c.lr_dev) {
     if (threadIdx.x == 0) {
       const double t = c.step_dev ? (double)*c.step_dev : (double)c.step;
@@ -384,11 +575,11 @@ __global__ void __launch_bounds__(ADAMW_THREADS, BITS == 32 ? MINB32 : MINB8) ad
       s_coef[1] = (float)(lr / (1.0 - pow(c.beta1, t)));
       s_coef[2] = (float)(1.0 / sqrt(1.0 - pow(c.beta2, t)));
     }
-    if (c.step_dev) c.step = (uint32_t)*c.step_dev;
+    if (c.step_dev) step = (uint32_t)*c.step_dev;
     __syncthreads();
-    c.keep = s_coef[0];
-    c.step_size = s_coef[1];
-    c.isb2 = s_coef[2];
+    keep_all = s_coef[0];
+    step_size = s_coef[1];
+    isb2 = s_coef[2];
   }
   if (c.max_norm > 0.0) {
     double s = 0.0;
@@ -409,129 +600,36 @@ __global__ void __launch_bounds__(ADAMW_THREADS, BITS == 32 ? MINB32 : MINB8) ad
     clip = s_clip;
     if (clip < 0.f) return;
   }
-  const uint32_t nb = tab.first[tab.count], stride = gridDim.x * ADAMW_WARPS;
-  uint32_t i = blockIdx.x * ADAMW_WARPS + warp;
-  int t = i < nb ? find_tensor(tab, nb - 1 - i) : 0;
-  for (; i < nb; i += stride) {
-    const uint32_t blk = nb - 1 - i;
-    while (blk < tab.first[t]) --t;
+  const uint32_t chunks = tab.first[tab.count];
+  for (uint32_t i = blockIdx.x; i < chunks; i += gridDim.x) {
+    // the tensor and the chunk are the block's: they and the pointers stay in uniform registers
+    const uint32_t chunk = chunks - 1 - i;
+    const int t = find_tensor(tab, chunk);
     const AdamwEntry& e = tab.e[t];
-    const uint32_t tb = blk - tab.first[t];  // block of the tensor
-    const long long base = (long long)tb * ADAMW_BLOCK;
-    const int left = (int)min(e.n - base, (long long)ADAMW_BLOCK);
-    const bool vec = (tab.flags[t] & AF_VEC) && left == ADAMW_BLOCK;
-    const float keep = (tab.flags[t] & AF_DECAY) ? c.keep : 1.f;
-    TP* pp = reinterpret_cast<TP*>(e.p) + base;
-    const TG* gp = reinterpret_cast<const TG*>(e.g) + base;
-    Raw8<TP> rp;
-    Raw8<TG> rg;
-    raw_load(pp, vec, left, lane, rp);
-    raw_load(reinterpret_cast<const TG*>(e.g) + base, vec, left, lane, rg);
-    float p[8];
+    const uint32_t tc = chunk - tab.first[t];  // chunk of the tensor
+    const long long base = (long long)tc * ADAMW_CHUNK;
+    const uint8_t flags = tab.flags[t];
+    Place<TP, TG, TS> a;
+    a.left = (int)min(e.n - base, (long long)ADAMW_CHUNK) - warp * ADAMW_BLOCK;
+    if (a.left <= 0) continue;
+    a.at = warp * ADAMW_BLOCK + lane * 8;
+    a.vec = (flags & AF_VEC) && a.left >= ADAMW_BLOCK;
+    a.p = reinterpret_cast<TP*>(e.p) + base;
+    a.g = reinterpret_cast<const TG*>(e.g) + base;
+    a.m = reinterpret_cast<TS*>(e.m) + base;
+    a.v = reinterpret_cast<TS*>(e.v) + base;
+    a.copy = e.copy ? e.copy + base : nullptr;
+    a.keep = (flags & AF_DECAY) ? keep_all : 1.f;
+    a.clip = clip;
+    a.isb2 = isb2;
+    a.step_size = step_size;
     if constexpr (BITS == 32) {
-      float m[8], v[8];
-      float* mp = reinterpret_cast<float*>(e.m) + base;
-      float* vp = reinterpret_cast<float*>(e.v) + base;
-      Raw8<float> rm, rv;
-      raw_load(mp, vec, left, lane, rm);
-      raw_load(vp, vec, left, lane, rv);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        p[j] = value(rp, j);
-        m[j] = value(rm, j);
-        v[j] = value(rv, j);
-        update1(c, keep, __fmul_rn(value(rg, j), clip), p[j], m[j], v[j]);
-      }
-      pack(m, rm);
-      pack(v, rv);
-      raw_store(mp, vec, left, lane, rm);
-      raw_store(vp, vec, left, lane, rv);
+      update32(c, a);
     } else {
-      uint8_t* mp = reinterpret_cast<uint8_t*>(e.m) + base;
-      uint8_t* vp = reinterpret_cast<uint8_t*>(e.v) + base;
-      const float ms = e.ms[tb], vs = e.vs[tb];
-      Raw8<uint8_t> rm, rv;
-      raw_load(mp, vec, left, lane, rm);
-      raw_load(vp, vec, left, lane, rv);
-      // 16 random bits of element k: half k % 8 of the draw of its octet k / 8; both moments take the same bits
-      // (each is right in the mean by itself, and the ratio's error is smaller when they round the same way)
-      const unsigned long long oct = (unsigned long long)tb * 32 + lane;
-      uint32_t r[4] = {(uint32_t)oct, (uint32_t)(oct >> 32), c.step, c.tensor0 + (uint32_t)t};
-      philox4x32_10(r, c.k0, c.k1);
-      if (!vec) {  // to the lanes that hold the elements
-        __syncwarp();
-        *reinterpret_cast<uint4*>(&rnd[warp][lane * 8]) = make_uint4(r[0], r[1], r[2], r[3]);
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) r[k] = rnd[warp][2 * k * 32 + lane] | (uint32_t)rnd[warp][(2 * k + 1) * 32 + lane] << 16;
-      }
-      // the usual case, two elements at a time: no zero and no large v, all finite
-      const f32x2 z = both(c.minus0);
-      f32x2 m2[4], v2[4], p2[4], nan2 = both(0.f);
-      float mx = 0.f;
-      uint32_t vx = 0, vmin = 0xffffffffu;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 x = decode_m2((rm.w[k >> 1] >> (16 * (k & 1))) & 0xffffu);
-        const float2 y = k & 1 ? decode_v2<1>(rv.w[k >> 1]) : decode_v2<0>(rv.w[k >> 1]);
-        const f32x2 g2 = mul2(pair(value(rg, 2 * k), value(rg, 2 * k + 1)), both(clip));
-        m2[k] = add2(product2(mul2(pair(x.x, x.y), both(ms)), both(c.b1), z), product2(g2, both(c.c1), z));
-        v2[k] = add2(product2(mul2(pair(y.x, y.y), both(vs)), both(c.b2), z), product2(mul2(g2, g2), both(c.c2), z));
-        nan2 = fma2(m2[k], both(0.f), nan2);  // NaN if an m is not finite
-        const float2 mm = halves(m2[k]), vv = halves(v2[k]);
-        mx = fmaxf(mx, fmaxf(fabsf(mm.x), fabsf(mm.y)));
-        vx = max(vx, max(__float_as_uint(vv.x), __float_as_uint(vv.y)));
-        vmin = min(vmin, min(__float_as_uint(vv.x), __float_as_uint(vv.y)));
-        // v 2^24 is a normal number whatever v > 0, and finite: v < 2^100 here
-        const float2 s2 = halves(mul2(v2[k], both(16777216.f)));
-        const float2 root = make_float2(sqrt_approx(s2.x), sqrt_approx(s2.y));
-        const float2 den = halves(fma2(pair(root.x, root.y), both(c.isb2 * 0x1p-12f), both(c.eps)));
-        const f32x2 q = mul2(m2[k], pair(rcp_approx(den.x), rcp_approx(den.y)));
-        p2[k] = fma2(q, both(-c.step_size), mul2(pair(value(rp, 2 * k), value(rp, 2 * k + 1)), both(keep)));
-      }
-      const float2 nn = halves(nan2);
-      uint32_t mxb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
-      vx = __reduce_max_sync(0xffffffffu, vx);
-      const bool odd = vmin == 0 || !(nn.x + nn.y == 0.f);
-      if (!__any_sync(0xffffffffu, odd) && vx < VX_USUAL && mxb < MX_USUAL) {
-        const uint32_t em = (uint32_t)max((int)(mxb >> 23) - 14, 0), ev = (uint32_t)max((int)(vx >> 23) - 29, 0);
-        // m / m_scale in two steps: the first takes the smallest normal code to 2^-126, so that what is below it is
-        // flushed to zero; the second back into the format's range (and -0 to 0)
-        const f32x2 down = both(__uint_as_float((127u + 127u - 120u - em - 7u) << 23)), up = both(0x1p120f);
-        const f32x2 vinv = both(__uint_as_float((254u - ev - 15u) << 23));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t u0 = (r[k] & 0xffffu) << 4, u1 = (r[k] >> 12) & 0xffff0u;
-          const float2 mm = halves(m2[k]), vv = halves(v2[k]);
-          const f32x2 mt = pair(__uint_as_float((__float_as_uint(mm.x) + u0) & 0xfff00000u),
-                                __uint_as_float((__float_as_uint(mm.y) + u1) & 0xfff00000u));
-          const f32x2 vt = pair(__uint_as_float((__float_as_uint(vv.x) + 2 * u0) & 0xffe00000u),
-                                __uint_as_float((__float_as_uint(vv.y) + 2 * u1) & 0xffe00000u));
-          const uint32_t mc = code_m2(fma2(mul2_ftz(mt, down), up, both(0.f)));
-          const float2 vy = halves(mul2(vt, vinv));
-          const uint32_t vc = code_v2(fmaxf(vy.x, 0x1p-14f), fmaxf(vy.y, 0x1p-14f));
-          rm.w[k >> 1] = k & 1 ? rm.w[k >> 1] | mc << 16 : mc;
-          rv.w[k >> 1] = k & 1 ? rv.w[k >> 1] | vc << 16 : vc;
-          const float2 pp2 = halves(p2[k]);
-          p[2 * k] = pp2.x;
-          p[2 * k + 1] = pp2.y;
-        }
-      } else {
-        general8(c, keep, clip, pp, gp, mp, vp, vec, left, lane, ms, vs, r, p, rm, rv, mxb, vx);
-      }
-      if (lane == 0) {
-        e.ms[tb] = mxb ? __uint_as_float((uint32_t)(max((int)(mxb >> 23) - 14, 0) + 7) << 23) : 0.f;
-        e.vs[tb] = vx ? __uint_as_float((uint32_t)(max((int)(vx >> 23) - 29, 0) + 15) << 23) : 0.f;
-      }
-      raw_store(mp, vec, left, lane, rm);
-      raw_store(vp, vec, left, lane, rv);
-    }
-    pack(p, rp);
-    raw_store(pp, vec, left, lane, rp);
-    if (e.copy) {
-      Raw8<uint16_t> rc;
-      pack(p, rc);
-      raw_store(e.copy + base, vec, left, lane, rc);
+      const uint32_t block = tc * ADAMW_WARPS + warp;  // of the tensor
+      a.ms = e.ms + block;
+      a.vs = e.vs + block;
+      update8(c, a, block, step, c.tensor0 + (uint32_t)t, lane, rnd[warp]);
     }
   }
   __threadfence();
@@ -541,10 +639,10 @@ __global__ void __launch_bounds__(ADAMW_THREADS, BITS == 32 ? MINB32 : MINB8) ad
 // host
 // ---------------------------------------------------------------------------
 template <typename... KArgs, typename... Args>
-cudaError_t launch(bool pdl, void (*kernel)(KArgs...), unsigned grid, cudaStream_t s, Args&&... args) {
+cudaError_t launch(bool pdl, void (*kernel)(KArgs...), unsigned grid, unsigned threads, cudaStream_t s, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(ADAMW_THREADS);
+  cfg.blockDim = dim3(threads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -554,17 +652,106 @@ cudaError_t launch(bool pdl, void (*kernel)(KArgs...), unsigned grid, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-typedef void (*AdamwFn)(const AdamwTable, const AdamwCoefs, const double*, int, float*);
-template <typename TP, typename TG>
-AdamwFn pick_bits(int bits) {
-  return bits == 32 ? adamw_kernel<TP, TG, 32> : adamw_kernel<TP, TG, 8>;
+template <int CAP>
+using AdamwFn = void (*)(const AdamwTable<CAP>, const AdamwCoefs, const double*, int, float*);
+template <int CAP, typename TP, typename TG>
+AdamwFn<CAP> pick_bits(int bits) {
+  return bits == 32 ? adamw_kernel<TP, TG, 32, CAP> : adamw_kernel<TP, TG, 8, CAP>;
 }
-AdamwFn pick(int pt, int gt, int bits) {
-  if (pt == SVLA_TYPE_F32) return gt == SVLA_TYPE_F32 ? pick_bits<float, float>(bits) : pick_bits<float, uint16_t>(bits);
-  return gt == SVLA_TYPE_F32 ? pick_bits<uint16_t, float>(bits) : pick_bits<uint16_t, uint16_t>(bits);
+template <int CAP>
+AdamwFn<CAP> pick(int pt, int gt, int bits) {
+  if (pt == SVLA_TYPE_F32)
+    return gt == SVLA_TYPE_F32 ? pick_bits<CAP, float, float>(bits) : pick_bits<CAP, float, uint16_t>(bits);
+  return gt == SVLA_TYPE_F32 ? pick_bits<CAP, uint16_t, float>(bits) : pick_bits<CAP, uint16_t, uint16_t>(bits);
+}
+
+// Blocks of a kernel that a device holds at once, asked for once a kernel and device.
+template <typename Fn>
+cudaError_t resident_blocks(Fn fn, int slot, unsigned* blocks) {
+  static std::atomic<unsigned> known[16][64];
+  int dev = 0, sms = 0, per_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (*blocks = known[slot][dev].load()) != 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, ADAMW_THREADS, 0);
+  if (e != cudaSuccess) return e;
+  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  *blocks = (unsigned)(per_sm * sms);
+  if (dev < 64) known[slot][dev].store(*blocks);
+  return cudaSuccess;
+}
+
+// Blocks of a step over `chunks`: what is resident at once, in as many waves as
+// leave every block 8 chunks, up to 16, with 32-bit moments: blocks that start
+// in order keep their accesses close together in memory, where ones that stay
+// drift apart (99.8 M values: 463 us in 13 waves, 509 in one). One wave with
+// 8-bit moments: the arithmetic bounds that step, and a block's start costs it
+// about 2 us (157 M bf16 values: 368 us in one wave, 395 in 4).
+unsigned step_blocks(unsigned chunks, unsigned resident, int bits) {
+  const unsigned waves = bits == 32 ? std::min(chunks / (8 * resident), 16u) : 1;
+  return std::min(chunks, resident * std::max(waves, 1u));
 }
 
 size_t launches_of(int n_tensors) { return ((size_t)n_tensors + ADAMW_CAP - 1) / ADAMW_CAP; }
+
+// The launches of a step: with a clip, pass 0 sums the squares of every launch's gradients; pass 1 updates.
+template <int CAP>
+svla_status adamw_launches(const svla_adamw_tensor* ts, int n, const svla_adamw_args* a, AdamwCoefs& c, double* workspace,
+                           float* grad_norm, cudaStream_t stream) {
+  const size_t pb = a->param_type == SVLA_TYPE_F32 ? 4 : 2, gb = a->grad_type == SVLA_TYPE_F32 ? 4 : 2;
+  const size_t sb = a->state_bits / 8;
+  const AdamwFn<CAP> fn = pick<CAP>(a->param_type, a->grad_type, a->state_bits);
+  unsigned resident = 0;
+  cudaError_t e = resident_blocks(fn, (CAP == ADAMW_FEW ? 8 : 0) | (pb == 2 ? 4 : 0) | (gb == 2 ? 2 : 0) | (sb == 1), &resident);
+  if (e != cudaSuccess) return svla_internal_fail(SVLA_ERR_CUDA, (std::string("adamw: ") + cudaGetErrorString(e)).c_str());
+  const std::unique_ptr<AdamwTable<CAP>> table(new AdamwTable<CAP>);
+  AdamwTable<CAP>& tab = *table;
+  const int launches = (n + CAP - 1) / CAP;
+  int n_partial = 0;
+  bool pdl = false;
+  for (int pass = a->max_norm > 0.0 ? 0 : 1; pass < 2; ++pass) {
+    for (int l = 0; l < launches; ++l) {
+      tab.count = std::min(CAP, n - l * CAP);
+      unsigned long long nb = 0;
+      for (int k = 0; k < tab.count; ++k) {
+        const svla_adamw_tensor& t = ts[l * CAP + k];
+        tab.e[k] = AdamwEntry{t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, reinterpret_cast<uint16_t*>(t.copy),
+                              (long long)t.n};
+        const bool vec = ((uintptr_t)t.param & (8 * pb - 1)) == 0 && ((uintptr_t)t.grad & (8 * gb - 1)) == 0 &&
+                         ((uintptr_t)t.copy & 15) == 0 && (((uintptr_t)t.m | (uintptr_t)t.v) & (8 * sb - 1)) == 0;
+        tab.flags[k] = (uint8_t)((t.decay ? AF_DECAY : 0) | (vec ? AF_VEC : 0));
+        tab.first[k] = (uint32_t)nb;
+        nb += (unsigned long long)((t.n + ADAMW_CHUNK - 1) / ADAMW_CHUNK);
+      }
+      if (nb > 0x7fffffffull) return svla_internal_fail(SVLA_ERR_SHAPE, "more than 2^42 elements in 400 tensors");
+      tab.first[tab.count] = (uint32_t)nb;
+      for (tab.shift = 0; (nb >> tab.shift) >= ADAMW_HINTS; ++tab.shift) {
+      }
+      for (int k = 0, at = 0; k <= ADAMW_HINTS; ++k) {
+        while (at + 1 < tab.count && tab.first[at + 1] <= (unsigned long long)k << tab.shift) ++at;
+        tab.hint[k] = (uint16_t)at;
+      }
+      const unsigned need = (unsigned)std::max(1ull, nb);
+      if (pass == 0) {
+        const unsigned grid = std::min((need + NORM_THREADS / ADAMW_THREADS - 1) / (NORM_THREADS / ADAMW_THREADS), (unsigned)NORM_BLOCKS);
+        double* part = workspace + n_partial;
+        e = a->grad_type == SVLA_TYPE_F32 ? launch(false, grad_norm_kernel<float, CAP>, grid, NORM_THREADS, stream, tab, part)
+                                          : launch(false, grad_norm_kernel<uint16_t, CAP>, grid, NORM_THREADS, stream, tab, part);
+        n_partial += (int)grid;
+        pdl = true;
+      } else {
+        c.tensor0 = (uint32_t)(l * CAP);
+        e = launch(pdl, fn, step_blocks(need, resident, a->state_bits), ADAMW_THREADS, stream, tab, c,
+                   (const double*)workspace, n_partial, l == 0 ? grad_norm : nullptr);
+        pdl = true;
+      }
+      if (e != cudaSuccess)
+        return svla_internal_fail(SVLA_ERR_CUDA, (std::string("adamw launch: ") + cudaGetErrorString(e)).c_str());
+    }
+  }
+  return SVLA_OK;
+}
 
 svla_status bad(svla_status s, int i, const char* why) {
   return svla_internal_fail(s, ((i < 0 ? std::string("workspace or grad_norm") : "tensor " + std::to_string(i)) + ": " + why).c_str());
@@ -645,10 +832,23 @@ svla_status adamw_checked(const svla_adamw_tensor* ts, int n, const svla_adamw_a
   c.b2 = (float)a->beta2;
   c.c2 = (float)(1.0 - a->beta2);
   c.eps = (float)a->eps;
-  c.minus0 = -0.f;
+  const auto two = [](float x) {
+    uint32_t b;
+    memcpy(&b, &x, 4);
+    return (unsigned long long)b << 32 | b;
+  };
+  c.b1_2 = two(c.b1);
+  c.c1_2 = two(c.c1);
+  c.b2_2 = two(c.b2);
+  c.c2_2 = two(c.c2);
+  c.eps_2 = two(c.eps);
+  c.minus0_2 = two(-0.f);
+  c.two24_2 = two(16777216.f);
+  for (uint32_t r = 0; r < 10; ++r) {
+    c.key[2 * r] = (uint32_t)a->seed + r * 0x9E3779B9u;
+    c.key[2 * r + 1] = (uint32_t)(a->seed >> 32) + r * 0xBB67AE85u;
+  }
   c.max_norm = a->max_norm;
-  c.k0 = (uint32_t)a->seed;
-  c.k1 = (uint32_t)(a->seed >> 32);
   c.step = (uint32_t)a->step;
   c.step_dev = reinterpret_cast<const long long*>(a->step_device);
   c.lr_dev = a->lr_device;
@@ -662,55 +862,9 @@ svla_status adamw_checked(const svla_adamw_tensor* ts, int n, const svla_adamw_a
     c.isb2 = (float)(1.0 / std::sqrt(1.0 - std::pow(a->beta2, (double)a->step)));
   }
 
-  const AdamwFn fn = pick(a->param_type, a->grad_type, a->state_bits);
-  int per_sm = 0, dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, ADAMW_THREADS, 0);
-  if (e != cudaSuccess || per_sm < 1)
-    return svla_internal_fail(SVLA_ERR_CUDA, (std::string("adamw: ") + cudaGetErrorString(e)).c_str());
-
-  // with a clip: pass 0 sums the squares of every launch's gradients, pass 1 updates
-  std::vector<AdamwTable> one(1);
-  AdamwTable& tab = one[0];
-  const int launches = (int)launches_of(n);
-  int n_partial = 0;
-  bool pdl = false;
-  for (int pass = clip ? 0 : 1; pass < 2; ++pass) {
-    for (int l = 0; l < launches; ++l) {
-      tab.count = std::min(ADAMW_CAP, n - l * ADAMW_CAP);
-      unsigned long long nb = 0;
-      for (int k = 0; k < tab.count; ++k) {
-        const svla_adamw_tensor& t = ts[l * ADAMW_CAP + k];
-        tab.e[k] = AdamwEntry{t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, reinterpret_cast<uint16_t*>(t.copy),
-                              (long long)t.n};
-        const bool vec = ((uintptr_t)t.param & (8 * pb - 1)) == 0 && ((uintptr_t)t.grad & (8 * gb - 1)) == 0 &&
-                         ((uintptr_t)t.copy & 15) == 0 && (((uintptr_t)t.m | (uintptr_t)t.v) & (8 * sb - 1)) == 0;
-        tab.flags[k] = (uint8_t)((t.decay ? AF_DECAY : 0) | (vec ? AF_VEC : 0));
-        tab.first[k] = (uint32_t)nb;
-        nb += (unsigned long long)((t.n + ADAMW_BLOCK - 1) / ADAMW_BLOCK);
-      }
-      if (nb > 0x7fffffffull) return svla_internal_fail(SVLA_ERR_SHAPE, "more than 2^39 elements in 400 tensors");
-      tab.first[tab.count] = (uint32_t)nb;
-      const unsigned need = (unsigned)std::max(1ull, (nb + ADAMW_WARPS - 1) / ADAMW_WARPS);
-      if (pass == 0) {
-        const unsigned grid = std::min(need, (unsigned)NORM_BLOCKS);
-        double* part = reinterpret_cast<double*>(workspace) + n_partial;
-        e = a->grad_type == SVLA_TYPE_F32 ? launch(false, grad_norm_kernel<float>, grid, stream, tab, part)
-                                          : launch(false, grad_norm_kernel<uint16_t>, grid, stream, tab, part);
-        n_partial += (int)grid;
-        pdl = true;
-      } else {
-        c.tensor0 = (uint32_t)(l * ADAMW_CAP);
-        e = launch(pdl, fn, std::min(need, (unsigned)(per_sm * sms)), stream, tab, c,
-                   reinterpret_cast<const double*>(workspace), n_partial, l == 0 ? grad_norm : nullptr);
-        pdl = true;
-      }
-      if (e != cudaSuccess)
-        return svla_internal_fail(SVLA_ERR_CUDA, (std::string("adamw launch: ") + cudaGetErrorString(e)).c_str());
-    }
-  }
-  return SVLA_OK;
+  double* ws = reinterpret_cast<double*>(workspace);
+  return n <= ADAMW_FEW ? adamw_launches<ADAMW_FEW>(ts, n, a, c, ws, grad_norm, stream)
+                        : adamw_launches<ADAMW_CAP>(ts, n, a, c, ws, grad_norm, stream);
 }
 
 }  // namespace

@@ -344,32 +344,44 @@ _TYPES = {torch.float32: _abi.TYPE_F32, torch.bfloat16: _abi.TYPE_BF16}
 
 
 def _type(t: torch.Tensor, what: str) -> int:
-    if t.dtype not in _TYPES:
+    kind = _TYPES.get(t.dtype)
+    if kind is None:
         raise ValueError(f"{what}: float32 or bfloat16 expected, got {t.dtype}")
-    return _TYPES[t.dtype]
+    return kind
 
 
-def _rows(t: torch.Tensor, shape, what: str):
-    """(pointer, type, row stride) of a [M, D] CUDA matrix whose rows are contiguous."""
-    if not t.is_cuda or tuple(t.shape) != tuple(shape) or (shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: a CUDA matrix of shape {tuple(shape)} with contiguous rows expected")
-    ld = t.stride(0) if shape[0] > 1 else shape[1]
-    if ld < shape[1]:
-        raise ValueError(f"{what}: rows overlap")
-    return ctypes.c_void_p(t.data_ptr()), _type(t, what), ld
+def _rows(t: torch.Tensor, M: int, D: int, device, what: str):
+    """(address, type, row stride) of a [M, D] CUDA matrix whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != D or t.device != device or not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA matrix of shape {(M, D)} on x's device expected")
+    ld, one = t.stride()
+    if M <= 1:
+        ld = D
+    if (D > 1 and one != 1) or ld < D:
+        raise ValueError(f"{what}: rows must be contiguous and apart")
+    return t.data_ptr(), _type(t, what), ld
 
 
-def _vec(t: Optional[torch.Tensor], n: int, what: str, dtype: Optional[torch.dtype] = None):
+def _vec(t: Optional[torch.Tensor], n: int, what: str, dtype: Optional[torch.dtype] = None, device=None):
     if t is None:
         return None
-    if not t.is_cuda or not t.is_contiguous() or t.numel() != n or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{what}: a contiguous CUDA tensor of {n} {dtype or 'float32 or bfloat16'} elements expected")
-    return ctypes.c_void_p(t.data_ptr())
+    if not t.is_cuda or not t.is_contiguous() or t.numel() != n or (dtype is not None and t.dtype != dtype) or (
+            device is not None and t.device != device):
+        raise ValueError(f"{what}: a contiguous CUDA tensor of {n} {dtype or 'float32 or bfloat16'} elements"
+                         f"{'' if device is None else f' on {device}'} expected")
+    return t.data_ptr()
 
 
-def _same_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
-    if any(o is not None and o.device != first.device for o in others):
-        raise ValueError("tensors are on different devices")
+def _launch(device, stream, fn, *args) -> int:
+    """fn(*args, stream) with `device` current, on `stream` or on the device's current one."""
+    if stream is not None:
+        raw = stream.cuda_stream
+    else:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, raw)
+    with torch.cuda.device(device):
+        return fn(*args, raw)
 
 
 def _scratch(nbytes: int, device, stream) -> Optional[torch.Tensor]:
@@ -390,15 +402,14 @@ def op_layernorm(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tens
     lib = _abi.load()
     if x.dim() != 2:
         raise ValueError("x: a [M, D] matrix expected")
-    M, D = x.shape
-    px, tx, ldx = _rows(x, (M, D), "x")
-    py, ty, ldy = _rows(y, (M, D), "y")
-    _same_device(x, gamma, beta, y, mean, rstd)
-    tw = _type(gamma, "gamma")
-    with torch.cuda.device(x.device):
-        _abi.check(lib.svla_op_layernorm(px, tx, ldx, _vec(gamma, D, "gamma"), _vec(beta, D, "beta", gamma.dtype), tw,
-                                         M, D, eps, py, ty, ldy, _vec(mean, M, "mean", torch.float32),
-                                         _vec(rstd, M, "rstd", torch.float32), _stream(stream)))
+    (M, D), dev, f32 = x.shape, x.device, torch.float32
+    px, tx, ldx = _rows(x, M, D, dev, "x")
+    py, ty, ldy = _rows(y, M, D, dev, "y")
+    st = _launch(dev, stream, lib.svla_op_layernorm, px, tx, ldx, _vec(gamma, D, "gamma", None, dev),
+                 _vec(beta, D, "beta", gamma.dtype, dev), _type(gamma, "gamma"), M, D, eps, py, ty, ldy,
+                 _vec(mean, M, "mean", f32, dev), _vec(rstd, M, "rstd", f32, dev))
+    if st:
+        _abi.check(st)
     return y
 
 
@@ -409,21 +420,22 @@ def op_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor
     lib = _abi.load()
     if x.dim() != 2:
         raise ValueError("x: a [M, D] matrix expected")
-    M, D = x.shape
-    px, tx, ldx = _rows(x, (M, D), "x")
-    pdy, ty, lddy = _rows(dy, (M, D), "dy")
-    pdx, tdx, lddx = _rows(dx, (M, D), "dx")
+    (M, D), dev, f32 = x.shape, x.device, torch.float32
+    px, tx, ldx = _rows(x, M, D, dev, "x")
+    pdy, ty, lddy = _rows(dy, M, D, dev, "dy")
+    pdx, tdx, lddx = _rows(dx, M, D, dev, "dx")
     if tdx != tx:
         raise ValueError("dx must have x's type")
-    _same_device(x, dy, gamma, mean, rstd, dx, dgamma, dbeta)
-    tw = _type(gamma, "gamma")
-    with torch.cuda.device(x.device):
-        n = int(lib.svla_op_layernorm_backward_workspace_bytes(M, D)) if dgamma is not None or dbeta is not None else 0
-        ws = _scratch(n, x.device, stream)
-        _abi.check(lib.svla_op_layernorm_backward(
-            pdy, ty, lddy, px, tx, ldx, _vec(gamma, D, "gamma"), tw, _vec(mean, M, "mean", torch.float32),
-            _vec(rstd, M, "rstd", torch.float32), M, D, pdx, lddx, _vec(dgamma, D, "dgamma", torch.float32),
-            _vec(dbeta, D, "dbeta", torch.float32), _ptr(ws), n, _stream(stream)))
+    n = 0
+    if dgamma is not None or dbeta is not None:
+        n = lib.svla_op_layernorm_backward_workspace_bytes(M, D)
+    ws = _scratch(n, dev, stream)
+    st = _launch(dev, stream, lib.svla_op_layernorm_backward, pdy, ty, lddy, px, tx, ldx,
+                 _vec(gamma, D, "gamma", None, dev), _type(gamma, "gamma"), _vec(mean, M, "mean", f32, dev),
+                 _vec(rstd, M, "rstd", f32, dev), M, D, pdx, lddx, _vec(dgamma, D, "dgamma", f32, dev),
+                 _vec(dbeta, D, "dbeta", f32, dev), None if ws is None else ws.data_ptr(), n)
+    if st:
+        _abi.check(st)
     return dx, dgamma, dbeta
 
 
@@ -479,64 +491,68 @@ class AdamW:
                 for what, x, d, c in (("m", self.m[i], kinds[0], k), ("v", self.v[i], kinds[1], k)) + (
                         () if state_bits == 32 else (("m_scale", self.m_scale[i], torch.float32, (k + 255) // 256),
                                                      ("v_scale", self.v_scale[i], torch.float32, (k + 255) // 256))):
-                    _vec(x, c, f"{what} of parameter {i}", d)
-                    _same_device(self.params[0], x)
+                    _vec(x, c, f"{what} of parameter {i}", d, dev)
         self.copies = [None] * n if copies is None else list(copies)
         flags = [True] * n if decay is None else [bool(d) for d in decay]
         if len(self.copies) != n or len(flags) != n or len(self.m) != n or len(self.v) != n:
             raise ValueError("copies, decay and state must have one entry a parameter")
-        self._size, self._grad_type = size, None
-        self._table = (_abi.SvlaAdamwTensor * n)()
-        for i, e in enumerate(self._table):
-            e.param, e.m, e.v, e.n, e.decay = self.params[i].data_ptr(), self.m[i].data_ptr(), self.v[i].data_ptr(), \
-                size[i], int(flags[i])
-            if state_bits == 8:
-                e.m_scale, e.v_scale = self.m_scale[i].data_ptr(), self.v_scale[i].data_ptr()
-            if self.copies[i] is not None:
-                _vec(self.copies[i], size[i], f"copy of parameter {i}", torch.bfloat16)
-                _same_device(self.params[0], self.copies[i])
-                e.copy = self.copies[i].data_ptr()
+        self._size = size
+        # the C table, as an array whose columns are filled at once
+        import numpy as np
+        self._table = np.zeros(n, dtype=np.dtype(_abi.SvlaAdamwTensor))
+        self._table_ptr = ctypes.cast(self._table.ctypes.data, ctypes.POINTER(_abi.SvlaAdamwTensor))
+        address = lambda ts: [0 if t is None else t.data_ptr() for t in ts]
+        for i, t in enumerate(self.copies):
+            _vec(t, size[i], f"copy of parameter {i}", torch.bfloat16, dev)
+        for column, ts in (("param", self.params), ("m", self.m), ("v", self.v), ("copy", self.copies)) + (
+                () if state_bits == 32 else (("m_scale", self.m_scale), ("v_scale", self.v_scale))):
+            self._table[column] = address(ts)
+        self._table["n"], self._table["decay"] = size, flags
         self.capturable = capturable
         self.step_tensor = torch.full((1,), self.steps, dtype=torch.int64, device=dev) if capturable else None
-        if isinstance(lr, torch.Tensor) and (not capturable or lr.dtype != torch.float64 or lr.device != dev
-                                             or lr.numel() != 1):
-            raise ValueError("a tensor lr: one float64 on the parameters' device, with capturable")
+        if isinstance(lr, torch.Tensor):
+            self._check_lr(lr)
         self.grad_norm = torch.zeros(1, device=dev) if max_norm else None
         ws = int(self.lib.svla_op_adamw_workspace_bytes(n)) if max_norm else 0
         self._ws = torch.empty(ws, dtype=torch.uint8, device=dev) if ws else None
         a = self._args = _abi.SvlaAdamwArgs()
         a.param_type, a.state_bits = _type(self.params[0], "parameters"), state_bits
         (a.beta1, a.beta2), a.eps, a.weight_decay, a.max_norm, a.seed = betas, eps, weight_decay, max_norm, seed
+        a.step_device = self.step_tensor.data_ptr() if capturable else None
+        self._args_ref, self._ws_bytes = ctypes.byref(a), ws
+        self._ws_ptr = self._ws.data_ptr() if ws else None
+        self._norm_ptr = self.grad_norm.data_ptr() if max_norm else None
+
+    def _check_lr(self, lr: torch.Tensor) -> None:
+        if not self.capturable or lr.dtype != torch.float64 or lr.device != self.device or lr.numel() != 1:
+            raise ValueError("a tensor lr: one float64 on the parameters' device, with capturable")
 
     def step(self, grads: Sequence[torch.Tensor], lr: Optional[float] = None, stream=None) -> None:
         """One step with these gradients (float32 or bfloat16, all one type, one contiguous tensor a parameter)."""
         if len(grads) != len(self._size):
             raise ValueError(f"{len(self._size)} gradients expected, got {len(grads)}")
-        dt = grads[0].dtype
-        for g, k, e in zip(grads, self._size, self._table):
-            if g.dtype != dt or g.device != self.device or g.numel() != k or not g.is_contiguous():
+        dt, dev = grads[0].dtype, self.device
+        for g, k in zip(grads, self._size):
+            if g.dtype != dt or g.device != dev or g.numel() != k or not g.is_contiguous():
                 raise ValueError("gradients: contiguous tensors of one type and the parameters' sizes, on their device")
-            e.grad = g.data_ptr()
+        self._table["grad"] = [g.data_ptr() for g in grads]
         a = self._args
         a.grad_type = _type(grads[0], "gradients")
+        a.step = self.steps + 1
         rate = self.lr if lr is None else lr
-        with torch.cuda.device(self.device):
+        if isinstance(rate, torch.Tensor):
+            self._check_lr(rate)
+            a.lr, a.lr_device = 0.0, rate.data_ptr()
+        else:
+            a.lr, a.lr_device = rate, None
+        if self.capturable:
+            on = stream if stream is not None else torch.cuda.current_stream(dev)
+            with torch.cuda.stream(on):
+                self.step_tensor.add_(1)
+        st = _launch(dev, stream, self.lib.svla_op_adamw, self._table_ptr, len(self._size), self._args_ref, self._ws_ptr,
+                     self._ws_bytes, self._norm_ptr)
+        if st:
             if self.capturable:
-                on = stream if stream is not None else torch.cuda.current_stream()
-                with torch.cuda.stream(on):
-                    self.step_tensor.add_(1)
-                a.step_device = self.step_tensor.data_ptr()
-                a.step = 1
-            else:
-                a.step = self.steps + 1
-            if isinstance(rate, torch.Tensor):
-                a.lr, a.lr_device = 0.0, rate.data_ptr()
-            else:
-                a.lr, a.lr_device = float(rate), None
-            st = self.lib.svla_op_adamw(self._table, len(self._size), ctypes.byref(a), _ptr(self._ws),
-                                        0 if self._ws is None else self._ws.numel(), _ptr(self.grad_norm),
-                                        _stream(stream))
-            if st != _abi.SVLA_OK and self.capturable:
                 with torch.cuda.stream(on):
                     self.step_tensor.sub_(1)
             _abi.check(st)
