@@ -11,7 +11,7 @@
 // elements each, T = 32 up to 1024 columns (the row's sums are shuffles of one
 // warp), else the fewest warps that hold a row in two units a thread. With VEC
 // a unit is 8 consecutive columns (16- and 32-byte accesses); else (an odd
-// width, stride or address) the columns j * T + thread.
+// width, stride or address) every 32nd one of its warp's 256.
 #include <algorithm>
 #include <exception>
 #include <string>
@@ -64,7 +64,7 @@ struct LnArgs {
   float* rstd;
   float* dgamma;
   float* dbeta;
-  float* partial;  // [blocks][2][D] where more than one block sums
+  float* partial;  // [blocks][2][slots] where more than one block sums
   int M, D, T;
   float eps, inv_d;
 };
@@ -72,7 +72,7 @@ struct LnArgs {
 // column of element k of unit u of this thread
 template <bool VEC>
 SVLA_DEV int column(int u, int k, int T, int tid) {
-  return VEC ? (u * T + tid) * 8 + k : (u * 8 + k) * T + tid;
+  return VEC ? (u * T + tid) * 8 + k : (u * T + (tid & ~31)) * 8 + k * 32 + (tid & 31);
 }
 
 // one row's elements of this thread as they lie in memory (zeros past the width)
@@ -118,7 +118,11 @@ struct RowRegs<E, NU, false> {
   E q[NU * 8];
   SVLA_DEV void load(const E* p, int D, int T, int tid) {
 #pragma unroll
-    for (int j = 0; j < NU * 8; ++j) q[j] = j * T + tid < D ? p[j * T + tid] : E(0);
+    for (int u = 0; u < NU; ++u) {
+      const int c = column<false>(u, 0, T, tid);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q[u * 8 + k] = c + k * 32 < D ? p[c + k * 32] : E(0);
+    }
   }
   SVLA_DEV float get(int u, int k) const { return load1(&q[u * 8 + k]); }
 };
@@ -130,26 +134,35 @@ SVLA_DEV void load_unit(const TW* w, int u, int D, int T, int tid, float (&x)[8]
     const int c = (u * T + tid) * 8;
     if (c < D) load8(w + c, x);
   } else {
+    const int c = column<false>(u, 0, T, tid);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = (u * 8 + k) * T + tid;
-      x[k] = c < D ? load1(w + c) : 0.f;
-    }
+    for (int k = 0; k < 8; ++k) x[k] = c + k * 32 < D ? load1(w + c + k * 32) : 0.f;
   }
 }
 
-// Sum over the T threads of a row: a butterfly of the warp, then (T > 32) the
-// warps' sums in order from shared memory. red: one float a warp of the block.
-SVLA_DEV float row_sum(float s, int T, float* red) {
+// Sums over the T threads of a row: a butterfly of the warp, then (T > 32) one
+// of the warps' sums, which every warp reads from shared memory. red: one float2
+// a warp of the block.
+template <int N>
+SVLA_DEV void row_sums(float (&s)[N], int T, float2* red) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (T == 32) return s;
-  const int warp = threadIdx.x >> 5, per = T >> 5, first = warp / per * per;
-  if ((threadIdx.x & 31) == 0) red[warp] = s;
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+  if (T == 32) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = T >> 5, first = warp / per * per;
+  if (lane == 0) red[warp] = make_float2(s[0], N > 1 ? s[N - 1] : 0.f);
   __syncthreads();
-  s = 0.f;
-  for (int w = 0; w < per; ++w) s += red[first + w];
-  return s;
+  const float2 v = lane < per ? red[first + lane] : make_float2(0.f, 0.f);
+  s[0] = v.x;
+  if (N > 1) s[N - 1] = v.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < per)
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = __shfl_sync(0xffffffffu, s[i], 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -158,7 +171,7 @@ SVLA_DEV float row_sum(float s, int T, float* red) {
 // ---------------------------------------------------------------------------
 template <typename TX, typename TY, typename TW, int NU, bool VEC>
 __global__ void __launch_bounds__(NU == 2 ? 1024 : 256) layernorm_kernel(const LnArgs a) {
-  __shared__ float red[2][32];
+  __shared__ float2 red[2][32];
   griddep_launch_dependents();
   griddep_wait();  // nothing is read before: the weights may come from an optimiser step
   const int T = a.T, tid = threadIdx.x % T, D = a.D;
@@ -166,21 +179,23 @@ __global__ void __launch_bounds__(NU == 2 ? 1024 : 256) layernorm_kernel(const L
   const bool active = row < a.M;
   RowRegs<TX, NU, VEC> x;
   x.load(reinterpret_cast<const TX*>(a.x) + (active ? row : 0) * a.ldx, D, T, tid);
-  float s = 0.f;
+  float s[1] = {0.f};
 #pragma unroll
   for (int u = 0; u < NU; ++u)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += x.get(u, k);
-  const float mean = row_sum(s, T, red[0]) * a.inv_d;
-  s = 0.f;
+    for (int k = 0; k < 8; ++k) s[0] += x.get(u, k);
+  row_sums(s, T, red[0]);
+  const float mean = s[0] * a.inv_d;
+  s[0] = 0.f;
 #pragma unroll
   for (int u = 0; u < NU; ++u)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float d = x.get(u, k) - mean;
-      if (column<VEC>(u, k, T, tid) < D) s = fmaf(d, d, s);
+      if (column<VEC>(u, k, T, tid) < D) s[0] = fmaf(d, d, s[0]);
     }
-  const float rstd = rsqrtf(row_sum(s, T, red[1]) * a.inv_d + a.eps);
+  row_sums(s, T, red[1]);
+  const float rstd = rsqrtf(s[0] * a.inv_d + a.eps);
   if (!active) return;
   TY* y = reinterpret_cast<TY*>(a.out) + row * a.ldo;
 #pragma unroll
@@ -194,11 +209,10 @@ __global__ void __launch_bounds__(NU == 2 ? 1024 : 256) layernorm_kernel(const L
       const int c = (u * T + tid) * 8;
       if (c < D) store8(y + c, o);
     } else {
+      const int c = column<false>(u, 0, T, tid);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int c = (u * 8 + k) * T + tid;
-        if (c < D) store1(y + c, o[k]);
-      }
+      for (int k = 0; k < 8; ++k)
+        if (c + k * 32 < D) store1(y + c + k * 32, o[k]);
     }
   }
   if (tid == 0) {
@@ -209,24 +223,35 @@ __global__ void __launch_bounds__(NU == 2 ? 1024 : 256) layernorm_kernel(const L
 
 // ---------------------------------------------------------------------------
 // backward: each group of T threads walks rows blockIdx.x * R + group, + grid *
-// R, .. and keeps its columns' sums of dgamma and dbeta; the next row is
-// loaded before the current one is reduced. At the end the groups of a block
-// add up in order in shared memory and the block's sums go to `partial` (or to
-// dgamma and dbeta, where there is one block).
+// R, .. and keeps its columns' sums of dgamma and dbeta; the next row is on its
+// way (VEC) while the current one is reduced. At the end the groups' sums are
+// added in order and go to `partial` (or to dgamma and dbeta, where there is one
+// block). Column sums are kept by slot, (u * 8 + k) * T + thread for element k
+// of unit u, so that neighbouring threads have neighbouring words.
 // ---------------------------------------------------------------------------
+template <bool VEC>
+SVLA_DEV int slot_column(int slot, int T) {
+  const int q = slot / T;
+  return column<VEC>(q >> 3, q & 7, T, slot - q * T);
+}
+
 template <typename TX, typename TY, typename TW, int NU, bool VEC, bool SMEM_ACC>
-__global__ void __launch_bounds__(SMEM_ACC ? 512 : NU > 2 ? 256 : 512)
+__global__ void __launch_bounds__(SMEM_ACC ? 512 : NU > 2 ? 256 : 512, SMEM_ACC ? 1 : NU > 2 ? 2 : 1)
     layernorm_bwd_kernel(const LnArgs a) {
-  extern __shared__ __align__(16) float cols[];  // [2][D] column sums of the block
-  __shared__ float red[2][2][16];
+  extern __shared__ __align__(16) float cols[];  // [R][2][slots] column sums (SMEM_ACC: [2][slots])
+  __shared__ float2 red[2][16];
+  // the next row's registers, where they leave two blocks an SM (16 warps)
+  constexpr int ROW = NU * 2 * (int)(sizeof(TX) + sizeof(TY));
+  constexpr bool PREFETCH = VEC && !SMEM_ACC && 2 * ROW + 16 * NU <= 96;
   griddep_launch_dependents();
   griddep_wait();
   const int T = a.T, tid = threadIdx.x % T, D = a.D, R = blockDim.x / T, group = threadIdx.x / T;
+  const int W = NU * 8 * T;  // slots
   const TX* xp = reinterpret_cast<const TX*>(a.x);
   const TY* dyp = reinterpret_cast<const TY*>(a.dy);
   float ag[SMEM_ACC ? 1 : NU * 8], ab[SMEM_ACC ? 1 : NU * 8];
   if constexpr (SMEM_ACC) {
-    for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) cols[c] = 0.f;
+    for (int c = threadIdx.x; c < 2 * W; c += blockDim.x) cols[c] = 0.f;
     __syncthreads();
   } else {
 #pragma unroll
@@ -245,15 +270,18 @@ __global__ void __launch_bounds__(SMEM_ACC ? 512 : NU > 2 ? 256 : 512)
     m = in ? a.mean[at] : 0.f;
     r = in ? a.rstd[at] : 0.f;
   };
-  fetch(row0 + group, x, dy, mean, rstd);
+  if (PREFETCH) fetch(row0 + group, x, dy, mean, rstd);
   for (int it = 0; row0 < a.M; row0 += stride, ++it) {
     const long long row = row0 + group;
     RowRegs<TX, NU, VEC> nx;
     RowRegs<TY, NU, VEC> ndy;
     float nmean = 0.f, nrstd = 0.f;
-    const bool more = !SMEM_ACC && row0 + stride < a.M;
-    if (more) fetch(row + stride, nx, ndy, nmean, nrstd);
-    float s0 = 0.f, s1 = 0.f;  // sums of w and of w xh
+    if (PREFETCH) {
+      if (row0 + stride < a.M) fetch(row + stride, nx, ndy, nmean, nrstd);
+    } else {
+      fetch(row, x, dy, mean, rstd);
+    }
+    float s[2] = {0.f, 0.f};  // sums of w and of w xh
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       float g[8] = {};
@@ -261,16 +289,20 @@ __global__ void __launch_bounds__(SMEM_ACC ? 512 : NU > 2 ? 256 : 512)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float d = dy.get(u, k), xh = (x.get(u, k) - mean) * rstd, w = d * g[k];
-        s0 += w;
-        s1 = fmaf(w, xh, s1);
-        if constexpr (!SMEM_ACC) {
+        s[0] += w;
+        s[1] = fmaf(w, xh, s[1]);
+        if constexpr (SMEM_ACC) {
+          float* c = cols + (u * 8 + k) * T + tid;
+          c[0] = fmaf(d, xh, c[0]);
+          c[W] += d;
+        } else {
           ag[u * 8 + k] = fmaf(d, xh, ag[u * 8 + k]);
           ab[u * 8 + k] += d;
         }
       }
     }
-    s0 = row_sum(s0, T, red[it & 1][0]) * a.inv_d;
-    s1 = row_sum(s1, T, red[it & 1][1]) * a.inv_d;
+    row_sums(s, T, red[it & 1]);
+    const float s0 = s[0] * a.inv_d, s1 = s[1] * a.inv_d;
     if (row < a.M) {
       TX* dx = reinterpret_cast<TX*>(a.out) + row * a.ldo;
 #pragma unroll
@@ -281,91 +313,71 @@ __global__ void __launch_bounds__(SMEM_ACC ? 512 : NU > 2 ? 256 : 512)
         for (int k = 0; k < 8; ++k) {
           const float xh = (x.get(u, k) - mean) * rstd, w = dy.get(u, k) * g[k];
           o[k] = rstd * (w - s0 - xh * s1);
-          if constexpr (SMEM_ACC) {
-            const int c = column<VEC>(u, k, T, tid);
-            if (c < D) {
-              cols[c] = fmaf(dy.get(u, k), xh, cols[c]);
-              cols[D + c] += dy.get(u, k);
-            }
-          }
         }
         if constexpr (VEC) {
           const int c = (u * T + tid) * 8;
           if (c < D) store8(dx + c, o);
         } else {
+          const int c = column<false>(u, 0, T, tid);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int c = (u * 8 + k) * T + tid;
-            if (c < D) store1(dx + c, o[k]);
-          }
+          for (int k = 0; k < 8; ++k)
+            if (c + k * 32 < D) store1(dx + c + k * 32, o[k]);
         }
       }
     }
-    if (more) {
+    if (PREFETCH) {
       x = nx;
       dy = ndy;
       mean = nmean;
       rstd = nrstd;
-    } else if (SMEM_ACC && row0 + stride < a.M) {
-      fetch(row + stride, x, dy, mean, rstd);
     }
   }
   if (!a.dgamma && !a.dbeta) return;
   if constexpr (!SMEM_ACC) {
-    for (int r = 0; r < R; ++r) {
-      if (group == r) {
+    float* mine = cols + (size_t)group * 2 * W + tid;
 #pragma unroll
-        for (int u = 0; u < NU; ++u)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int c = column<VEC>(u, k, T, tid);
-            if (c < D) {
-              cols[c] = r ? cols[c] + ag[u * 8 + k] : ag[u * 8 + k];
-              cols[D + c] = r ? cols[D + c] + ab[u * 8 + k] : ab[u * 8 + k];
-            }
-          }
-      }
-      __syncthreads();
+    for (int j = 0; j < NU * 8; ++j) {
+      mine[j * T] = ag[j];
+      mine[W + j * T] = ab[j];
     }
-  } else {
-    __syncthreads();
   }
-  if (gridDim.x == 1) {
-    for (int c = threadIdx.x; c < D; c += blockDim.x) {
-      if (a.dgamma) a.dgamma[c] = cols[c];
-      if (a.dbeta) a.dbeta[c] = cols[D + c];
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * W; c += blockDim.x) {
+    float v = cols[c];
+    if constexpr (!SMEM_ACC)
+      for (int r = 1; r < R; ++r) v += cols[(size_t)r * 2 * W + c];
+    if (gridDim.x > 1) {
+      a.partial[(size_t)blockIdx.x * 2 * W + c] = v;
+    } else {
+      const int col = slot_column<VEC>(c < W ? c : c - W, T);
+      float* out = c < W ? a.dgamma : a.dbeta;
+      if (out && col < D) out[col] = v;
     }
-  } else {
-    float* out = a.partial + (size_t)blockIdx.x * 2 * D;
-    for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) out[c] = cols[c];
   }
 }
 
-// dgamma and dbeta: the blocks' partial sums added per column. A block of 32
-// columns; thread row j adds the blocks j, j + 32, .. and the 32 sums are
-// added in order.
-__global__ void __launch_bounds__(1024) layernorm_cols_kernel(const float* partial, int blocks, int D, float* dgamma,
-                                                              float* dbeta) {
+// dgamma and dbeta: the blocks' partial sums added per slot. A block of 32
+// slots; thread row j adds the blocks j, j + 32, .. and the 32 sums are added in
+// order.
+template <bool VEC>
+__global__ void __launch_bounds__(1024) layernorm_cols_kernel(const float* partial, int blocks, int D, int W, int T,
+                                                              float* dgamma, float* dbeta) {
   __shared__ float part[32][33];
   griddep_launch_dependents();
   griddep_wait();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
-  if (c < 2 * D) {
 #pragma unroll 10
-    for (int b = threadIdx.y; b < blocks; b += 32) s += partial[(size_t)b * 2 * D + c];
-  }
+  for (int b = threadIdx.y; b < blocks; b += 32) s += partial[(size_t)b * 2 * W + c];
   part[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.y == 0 && c < 2 * D) {
+  if (threadIdx.y == 0) {
     s = 0.f;
 #pragma unroll
     for (int j = 0; j < 32; ++j) s += part[j][threadIdx.x];
-    if (c < D) {
-      if (dgamma) dgamma[c] = s;
-    } else if (dbeta) {
-      dbeta[c - D] = s;
-    }
+    const int col = slot_column<VEC>(c < W ? c : c - W, T);
+    float* out = c < W ? dgamma : dbeta;
+    if (out && col < D) out[col] = s;
   }
 }
 
@@ -459,13 +471,14 @@ svla_status run(LnArgs& a, int xt, int yt, int wt, bool bwd, bool vec, cudaStrea
   const bool smem_acc = bwd && a.D > LN_SMEM_ACC_D;
   const LnFn fn = pick(xt, yt, wt, bwd, vec, p.NU, smem_acc);
   const int blocks = bwd ? ln_bwd_blocks(a.M, p) : (a.M + p.R - 1) / p.R;
-  const size_t smem = bwd && (smem_acc || a.dgamma || a.dbeta) ? (size_t)2 * a.D * sizeof(float) : 0;
+  const int W = p.NU * 8 * p.T;
+  const size_t smem = bwd && (smem_acc || a.dgamma || a.dbeta) ? (size_t)(smem_acc ? 1 : p.R) * 2 * W * sizeof(float) : 0;
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess) e = launch(fn, dim3(blocks), dim3(p.threads), smem, s, a);
   if (e == cudaSuccess && bwd && blocks > 1 && (a.dgamma || a.dbeta))
-    e = launch(layernorm_cols_kernel, dim3((2 * a.D + 31) / 32), dim3(32, 32), 0, s, (const float*)a.partial, blocks,
-               a.D, a.dgamma, a.dbeta);
+    e = launch(vec ? layernorm_cols_kernel<true> : layernorm_cols_kernel<false>, dim3(2 * W / 32), dim3(32, 32), 0, s,
+               (const float*)a.partial, blocks, a.D, W, p.T, a.dgamma, a.dbeta);
   if (e != cudaSuccess)
     return svla_internal_fail(SVLA_ERR_CUDA, (std::string("layernorm launch: ") + cudaGetErrorString(e)).c_str());
   return SVLA_OK;
@@ -520,8 +533,9 @@ svla_status svla_op_layernorm(const void* x, int x_type, int ldx, const void* ga
 
 size_t svla_op_layernorm_backward_workspace_bytes(int M, int D) {
   if (M < 1 || D < 1 || D > svla::LN_MAX_D) return 0;
-  const int blocks = svla::ln_bwd_blocks(M, svla::ln_plan(D, true));
-  return blocks > 1 ? (size_t)blocks * 2 * D * sizeof(float) : 0;
+  const svla::LnPlan p = svla::ln_plan(D, true);
+  const int blocks = svla::ln_bwd_blocks(M, p);
+  return blocks > 1 ? (size_t)blocks * 2 * p.NU * 8 * p.T * sizeof(float) : 0;
 }
 
 svla_status svla_op_layernorm_backward(const void* dy, int y_type, int lddy, const void* x, int x_type, int ldx,
