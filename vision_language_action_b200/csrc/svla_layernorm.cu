@@ -8,10 +8,10 @@
 //   dx = r (w - mean(w) - xh mean(w xh)),  dgamma = sum dy xh,  dbeta = sum dy
 //
 // Both passes read each row once into registers: T threads hold NU units of 8
-// elements each, T = 32 up to 1024 columns (the row's sums are shuffles of one
-// warp), else the fewest warps that hold a row in two units a thread. With VEC
-// a unit is 8 consecutive columns (16- and 32-byte accesses); else (an odd
-// width, stride or address) every 32nd one of its warp's 256.
+// elements each. Narrow rows (up to 128 columns) take a part of a warp, T = 1 to
+// 16; wider ones whole warps. With VEC a unit is 8 consecutive columns (16- and
+// 32-byte accesses); else (an odd width, stride or address) every 32nd (narrow:
+// T-th) one.
 #include <algorithm>
 #include <exception>
 #include <string>
@@ -27,31 +27,56 @@ namespace {
 
 constexpr int LN_MAX_D = 16384;
 constexpr int LN_BWD_BLOCKS = 296;  // blocks (partial sums of dgamma and dbeta): 2 on each of 148 SMs
-constexpr int LN_SMEM_ACC_D = 8192; // wider rows keep the column sums in shared memory
 
 struct LnPlan {
   int T, NU, R, threads;  // threads a row, units a thread, rows a block, threads a block
+  bool smem_acc;          // the backward's column sums in shared memory
 };
 
-LnPlan ln_plan(int D, bool backward) {
+// max_nu: units a thread may hold (the registers of its row, and in the backward of its columns' sums)
+LnPlan ln_plan(int D, int max_nu, int max_t) {
   LnPlan p;
   const int units = (D + 7) / 8;
-  if (units <= 128) {
-    p.T = 32;
-    p.NU = (units + 31) / 32;
-  } else if (backward && D > LN_SMEM_ACC_D) {
-    p.T = 512;
-    p.NU = 4;
+  p.smem_acc = false;
+  if (units <= 16) {
+    p.T = 1;
+    while (p.T < units) p.T *= 2;
+    p.NU = 1;
   } else {
-    p.T = 32 * ((units + 63) / 64);
-    p.NU = 2;
+    p.T = 32 * ((units + 32 * max_nu - 1) / (32 * max_nu));
+    p.NU = (units + p.T - 1) / p.T;
+    if (p.T > max_t) {
+      p.T = max_t;
+      p.NU = 4;  // 4 units x 512 threads hold the widest row
+      p.smem_acc = true;
+    }
   }
   p.R = std::max(1, 256 / p.T);
   p.threads = p.R * p.T;
   return p;
 }
+// Forward: one warp a row up to 1024 columns, then two units a thread (up to 1024 threads a row). Rows of bf16 without
+// the wide accesses are bound by the number of 2-byte accesses in flight: one unit a thread from 257 columns up (30000
+// rows of 1283: 81 us, 116 with two; fp32 rows 79 with one, 69 with two).
+LnPlan ln_fwd_plan(int D, bool vec, bool bf16_x) {
+  if (!vec && bf16_x && D > 256) return ln_plan(D, D <= 8192 ? 1 : 2, 1024);
+  return D <= 1024 ? ln_plan(D, 4, 32) : ln_plan(D, 2, 1024);
+}
+// Backward: 16 sums and, per unit, 4 (bf16) or 8 (fp32) registers of x and of dy, beside the rest in the 128
+// registers of 512 threads an SM. One warp a row up to 1024 columns; two units a thread while 512 threads hold the
+// row so (the next row's registers fit beside it); then three or, of bf16 rows, four. What is wider keeps its columns'
+// sums in shared memory.
+LnPlan ln_bwd_plan(int D, bool bf16_rows) {
+  if (D <= 1024) return ln_plan(D, 4, 32);
+  return ln_plan(D, D <= 8192 ? 2 : D <= 12288 ? 3 : bf16_rows ? 4 : 3, 512);
+}
 
 int ln_bwd_blocks(int M, const LnPlan& p) { return std::min((M + p.R - 1) / p.R, LN_BWD_BLOCKS); }
+size_t ln_bwd_workspace(int M, int D, bool bf16_rows) {
+  const LnPlan p = ln_bwd_plan(D, bf16_rows);
+  const int blocks = ln_bwd_blocks(M, p);
+  return blocks > 1 ? (size_t)blocks * 2 * p.NU * 8 * p.T * sizeof(float) : 0;
+}
 
 struct LnArgs {
   const void* x;
@@ -69,17 +94,21 @@ struct LnArgs {
   float eps, inv_d;
 };
 
-// column of element k of unit u of this thread
-template <bool VEC>
+// Column of element k of unit u of this thread. STEP: 0 with VEC; else the
+// distance of a thread's columns, 32, or T where T is below 32 (STEP 1).
+enum { VEC8 = 0, STEP_T = 1, STEP_32 = 2 };
+template <int STEP>
 SVLA_DEV int column(int u, int k, int T, int tid) {
-  return VEC ? (u * T + tid) * 8 + k : (u * T + (tid & ~31)) * 8 + k * 32 + (tid & 31);
+  if constexpr (STEP == VEC8) return (u * T + tid) * 8 + k;
+  if constexpr (STEP == STEP_T) return k * T + tid;
+  return (u * T + (tid & ~31)) * 8 + k * 32 + (tid & 31);
 }
 
 // one row's elements of this thread as they lie in memory (zeros past the width)
-template <typename E, int NU, bool VEC>
+template <typename E, int NU, int STEP>
 struct RowRegs;
 template <int NU>
-struct RowRegs<float, NU, true> {
+struct RowRegs<float, NU, VEC8> {
   float4 q[2 * NU];
   SVLA_DEV void load(const float* p, int D, int T, int tid) {
 #pragma unroll
@@ -98,7 +127,7 @@ struct RowRegs<float, NU, true> {
   }
 };
 template <int NU>
-struct RowRegs<uint16_t, NU, true> {
+struct RowRegs<uint16_t, NU, VEC8> {
   uint4 q[NU];
   SVLA_DEV void load(const uint16_t* p, int D, int T, int tid) {
 #pragma unroll
@@ -113,107 +142,161 @@ struct RowRegs<uint16_t, NU, true> {
     return __uint_as_float((k & 1) ? (w & 0xffff0000u) : (w << 16));
   }
 };
-template <typename E, int NU>
-struct RowRegs<E, NU, false> {
+template <typename E, int NU, int STEP>
+struct RowRegs {
   E q[NU * 8];
   SVLA_DEV void load(const E* p, int D, int T, int tid) {
+    const int step = STEP == STEP_T ? T : 32;
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const int c = column<false>(u, 0, T, tid);
+      const int c = column<STEP>(u, 0, T, tid);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[u * 8 + k] = c + k * 32 < D ? p[c + k * 32] : E(0);
+      for (int k = 0; k < 8; ++k) q[u * 8 + k] = c + k * step < D ? p[c + k * step] : E(0);
     }
   }
   SVLA_DEV float get(int u, int k) const { return load1(&q[u * 8 + k]); }
 };
 
 // columns of a vector of weights into 8 floats of unit u
-template <typename TW, bool VEC>
+template <typename TW, int STEP>
 SVLA_DEV void load_unit(const TW* w, int u, int D, int T, int tid, float (&x)[8]) {
-  if constexpr (VEC) {
-    const int c = (u * T + tid) * 8;
+  const int c = column<STEP>(u, 0, T, tid);
+  if constexpr (STEP == VEC8) {
     if (c < D) load8(w + c, x);
   } else {
-    const int c = column<false>(u, 0, T, tid);
+    const int step = STEP == STEP_T ? T : 32;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = c + k * 32 < D ? load1(w + c + k * 32) : 0.f;
+    for (int k = 0; k < 8; ++k) x[k] = c + k * step < D ? load1(w + c + k * step) : 0.f;
+  }
+}
+template <typename E, int STEP>
+SVLA_DEV void store_unit(E* p, int u, int D, int T, int tid, const float (&x)[8]) {
+  const int c = column<STEP>(u, 0, T, tid);
+  if constexpr (STEP == VEC8) {
+    if (c < D) store8(p + c, x);
+  } else {
+    const int step = STEP == STEP_T ? T : 32;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c + k * step < D) store1(p + c + k * step, x[k]);
   }
 }
 
-// Sums over the T threads of a row: a butterfly of the warp, then (T > 32) one
-// of the warps' sums, which every warp reads from shared memory. red: one float2
-// a warp of the block.
-template <int N>
-SVLA_DEV void row_sums(float (&s)[N], int T, float2* red) {
+// Sums over the T threads of a row: a butterfly of the warp or of its part, then
+// (T > 32) one of the warps' sums, which every warp reads from shared memory.
+// red: one float2 a warp of the block.
+SVLA_DEV void row_sums(float& s0, float& s1, int T, float2* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-  if (T == 32) return;
+    if (o < T) {
+      s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+    }
+  if (T <= 32) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = T >> 5, first = warp / per * per;
-  if (lane == 0) red[warp] = make_float2(s[0], N > 1 ? s[N - 1] : 0.f);
+  if (lane == 0) red[warp] = make_float2(s0, s1);
   __syncthreads();
   const float2 v = lane < per ? red[first + lane] : make_float2(0.f, 0.f);
-  s[0] = v.x;
-  if (N > 1) s[N - 1] = v.y;
+  s0 = v.x;
+  s1 = v.y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    if (o < per)
-#pragma unroll
-      for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-#pragma unroll
-  for (int i = 0; i < N; ++i) s[i] = __shfl_sync(0xffffffffu, s[i], 0);
+    if (o < per) {
+      s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+    }
+  s0 = __shfl_sync(0xffffffffu, s0, 0);
+  s1 = __shfl_sync(0xffffffffu, s1, 0);
 }
 
+// Mean and sum of squared differences of two sets of values from theirs (Chan,
+// Golub and LeVeque 1979): no cancellation of large sums, in one pass.
+struct Moments {
+  float n, mean, m2;
+  SVLA_DEV void merge(const Moments& o) {
+    const float all = n + o.n, part = all > 0.f ? __fdividef(o.n, all) : 0.f, d = o.mean - mean;
+    mean = fmaf(d, part, mean);
+    m2 = m2 + o.m2 + d * d * n * part;
+    n = all;
+  }
+  SVLA_DEV void merge_lanes(int from, int below) {  // butterfly over distances from .. 1 that are below `below`
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o <= from && o < below) {
+        Moments x;
+        x.n = __shfl_xor_sync(0xffffffffu, n, o);
+        x.mean = __shfl_xor_sync(0xffffffffu, mean, o);
+        x.m2 = __shfl_xor_sync(0xffffffffu, m2, o);
+        merge(x);
+      }
+  }
+};
+
 // ---------------------------------------------------------------------------
-// forward: one row a group of T threads; mean first, then the squares of the
-// differences from registers (no cancellation of two large sums)
+// forward: one row a group of T threads. A row of one warp or a part of one:
+// mean first, then the squares of the differences from registers. Of several
+// warps: each warp so for its columns, then the warps' moments merged, for one
+// barrier a row.
 // ---------------------------------------------------------------------------
-template <typename TX, typename TY, typename TW, int NU, bool VEC>
-__global__ void __launch_bounds__(NU == 2 ? 1024 : 256) layernorm_kernel(const LnArgs a) {
-  __shared__ float2 red[2][32];
+template <typename TX, typename TY, typename TW, int NU, int STEP>
+__global__ void __launch_bounds__(NU <= 2 ? 1024 : 256) layernorm_kernel(const LnArgs a) {
+  __shared__ Moments red[32];
   griddep_launch_dependents();
   griddep_wait();  // nothing is read before: the weights may come from an optimiser step
   const int T = a.T, tid = threadIdx.x % T, D = a.D;
   const long long row = (long long)blockIdx.x * (blockDim.x / T) + threadIdx.x / T;
   const bool active = row < a.M;
-  RowRegs<TX, NU, VEC> x;
+  RowRegs<TX, NU, STEP> x;
   x.load(reinterpret_cast<const TX*>(a.x) + (active ? row : 0) * a.ldx, D, T, tid);
-  float s[1] = {0.f};
+  // columns of this thread's warp (or part of one): whole units of 256, the last one cut
+  const int width = min(T, 32);
+  float cnt = (float)D, inv_cnt = a.inv_d;
+  if (T > 32) {
+    int mine = 0;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) mine += max(0, min(256, D - (u * T + (tid & ~31)) * 8));
+    cnt = (float)mine;
+    inv_cnt = mine ? 1.f / cnt : 0.f;
+  }
+  float s = 0.f;
 #pragma unroll
   for (int u = 0; u < NU; ++u)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s[0] += x.get(u, k);
-  row_sums(s, T, red[0]);
-  const float mean = s[0] * a.inv_d;
-  s[0] = 0.f;
+    for (int k = 0; k < 8; ++k) s += x.get(u, k);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < width) s += __shfl_xor_sync(0xffffffffu, s, o);
+  float mean = s * inv_cnt, m2 = 0.f;
 #pragma unroll
   for (int u = 0; u < NU; ++u)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float d = x.get(u, k) - mean;
-      if (column<VEC>(u, k, T, tid) < D) s[0] = fmaf(d, d, s[0]);
+      if (column<STEP>(u, k, T, tid) < D) m2 = fmaf(d, d, m2);
     }
-  row_sums(s, T, red[1]);
-  const float rstd = rsqrtf(s[0] * a.inv_d + a.eps);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < width) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+  if (T > 32) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = T >> 5, first = warp / per * per;
+    if (lane == 0) red[warp] = Moments{cnt, mean, m2};
+    __syncthreads();
+    Moments all = lane < per ? red[first + lane] : Moments{0.f, 0.f, 0.f};
+    all.merge_lanes(16, per);
+    mean = __shfl_sync(0xffffffffu, all.mean, 0);
+    m2 = __shfl_sync(0xffffffffu, all.m2, 0);
+  }
+  const float rstd = rsqrtf(m2 * a.inv_d + a.eps);
   if (!active) return;
   TY* y = reinterpret_cast<TY*>(a.out) + row * a.ldo;
 #pragma unroll
   for (int u = 0; u < NU; ++u) {
     float g[8], b[8] = {}, o[8];
-    load_unit<TW, VEC>(reinterpret_cast<const TW*>(a.gamma), u, D, T, tid, g);
-    if (a.beta) load_unit<TW, VEC>(reinterpret_cast<const TW*>(a.beta), u, D, T, tid, b);
+    load_unit<TW, STEP>(reinterpret_cast<const TW*>(a.gamma), u, D, T, tid, g);
+    if (a.beta) load_unit<TW, STEP>(reinterpret_cast<const TW*>(a.beta), u, D, T, tid, b);
 #pragma unroll
     for (int k = 0; k < 8; ++k) o[k] = fmaf((x.get(u, k) - mean) * rstd, g[k], b[k]);
-    if constexpr (VEC) {
-      const int c = (u * T + tid) * 8;
-      if (c < D) store8(y + c, o);
-    } else {
-      const int c = column<false>(u, 0, T, tid);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + k * 32 < D) store1(y + c + k * 32, o[k]);
-    }
+    store_unit<TY, STEP>(y, u, D, T, tid, o);
   }
   if (tid == 0) {
     if (a.mean) a.mean[row] = mean;
@@ -229,20 +312,20 @@ __global__ void __launch_bounds__(NU == 2 ? 1024 : 256) layernorm_kernel(const L
 // block). Column sums are kept by slot, (u * 8 + k) * T + thread for element k
 // of unit u, so that neighbouring threads have neighbouring words.
 // ---------------------------------------------------------------------------
-template <bool VEC>
+template <int STEP>
 SVLA_DEV int slot_column(int slot, int T) {
   const int q = slot / T;
-  return column<VEC>(q >> 3, q & 7, T, slot - q * T);
+  return column<STEP>(q >> 3, q & 7, T, slot - q * T);
 }
 
-template <typename TX, typename TY, typename TW, int NU, bool VEC, bool SMEM_ACC>
-__global__ void __launch_bounds__(SMEM_ACC ? 512 : NU > 2 ? 256 : 512, SMEM_ACC ? 1 : NU > 2 ? 2 : 1)
+template <typename TX, typename TY, typename TW, int NU, int STEP, bool SMEM_ACC>
+__global__ void __launch_bounds__(STEP == STEP_T ? 256 : 512)
     layernorm_bwd_kernel(const LnArgs a) {
   extern __shared__ __align__(16) float cols[];  // [R][2][slots] column sums (SMEM_ACC: [2][slots])
   __shared__ float2 red[2][16];
   // the next row's registers, where they leave two blocks an SM (16 warps)
   constexpr int ROW = NU * 2 * (int)(sizeof(TX) + sizeof(TY));
-  constexpr bool PREFETCH = VEC && !SMEM_ACC && 2 * ROW + 16 * NU <= 96;
+  constexpr bool PREFETCH = STEP == VEC8 && !SMEM_ACC && 2 * ROW + 16 * NU <= 80;
   griddep_launch_dependents();
   griddep_wait();
   const int T = a.T, tid = threadIdx.x % T, D = a.D, R = blockDim.x / T, group = threadIdx.x / T;
@@ -259,10 +342,10 @@ __global__ void __launch_bounds__(SMEM_ACC ? 512 : NU > 2 ? 256 : 512, SMEM_ACC 
   }
   const long long stride = (long long)gridDim.x * R;
   long long row0 = (long long)blockIdx.x * R;
-  RowRegs<TX, NU, VEC> x;
-  RowRegs<TY, NU, VEC> dy;
+  RowRegs<TX, NU, STEP> x;
+  RowRegs<TY, NU, STEP> dy;
   float mean = 0.f, rstd = 0.f;
-  auto fetch = [&](long long row, RowRegs<TX, NU, VEC>& fx, RowRegs<TY, NU, VEC>& fy, float& m, float& r) {
+  auto fetch = [&](long long row, RowRegs<TX, NU, STEP>& fx, RowRegs<TY, NU, STEP>& fy, float& m, float& r) {
     const bool in = row < a.M;
     const long long at = in ? row : 0;
     fx.load(xp + at * a.ldx, in ? D : 0, T, tid);
@@ -273,24 +356,24 @@ __global__ void __launch_bounds__(SMEM_ACC ? 512 : NU > 2 ? 256 : 512, SMEM_ACC 
   if (PREFETCH) fetch(row0 + group, x, dy, mean, rstd);
   for (int it = 0; row0 < a.M; row0 += stride, ++it) {
     const long long row = row0 + group;
-    RowRegs<TX, NU, VEC> nx;
-    RowRegs<TY, NU, VEC> ndy;
+    RowRegs<TX, NU, STEP> nx;
+    RowRegs<TY, NU, STEP> ndy;
     float nmean = 0.f, nrstd = 0.f;
     if (PREFETCH) {
       if (row0 + stride < a.M) fetch(row + stride, nx, ndy, nmean, nrstd);
     } else {
       fetch(row, x, dy, mean, rstd);
     }
-    float s[2] = {0.f, 0.f};  // sums of w and of w xh
+    float s0 = 0.f, s1 = 0.f;  // sums of w and of w xh
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       float g[8] = {};
-      load_unit<TW, VEC>(reinterpret_cast<const TW*>(a.gamma), u, D, T, tid, g);
+      load_unit<TW, STEP>(reinterpret_cast<const TW*>(a.gamma), u, D, T, tid, g);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float d = dy.get(u, k), xh = (x.get(u, k) - mean) * rstd, w = d * g[k];
-        s[0] += w;
-        s[1] = fmaf(w, xh, s[1]);
+        s0 += w;
+        s1 = fmaf(w, xh, s1);
         if constexpr (SMEM_ACC) {
           float* c = cols + (u * 8 + k) * T + tid;
           c[0] = fmaf(d, xh, c[0]);
@@ -301,28 +384,21 @@ __global__ void __launch_bounds__(SMEM_ACC ? 512 : NU > 2 ? 256 : 512, SMEM_ACC 
         }
       }
     }
-    row_sums(s, T, red[it & 1]);
-    const float s0 = s[0] * a.inv_d, s1 = s[1] * a.inv_d;
+    row_sums(s0, s1, T, red[it & 1]);
+    s0 *= a.inv_d;
+    s1 *= a.inv_d;
     if (row < a.M) {
       TX* dx = reinterpret_cast<TX*>(a.out) + row * a.ldo;
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
         float g[8] = {}, o[8];
-        load_unit<TW, VEC>(reinterpret_cast<const TW*>(a.gamma), u, D, T, tid, g);
+        load_unit<TW, STEP>(reinterpret_cast<const TW*>(a.gamma), u, D, T, tid, g);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float xh = (x.get(u, k) - mean) * rstd, w = dy.get(u, k) * g[k];
           o[k] = rstd * (w - s0 - xh * s1);
         }
-        if constexpr (VEC) {
-          const int c = (u * T + tid) * 8;
-          if (c < D) store8(dx + c, o);
-        } else {
-          const int c = column<false>(u, 0, T, tid);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (c + k * 32 < D) store1(dx + c + k * 32, o[k]);
-        }
+        store_unit<TX, STEP>(dx, u, D, T, tid, o);
       }
     }
     if (PREFETCH) {
@@ -349,7 +425,7 @@ __global__ void __launch_bounds__(SMEM_ACC ? 512 : NU > 2 ? 256 : 512, SMEM_ACC 
     if (gridDim.x > 1) {
       a.partial[(size_t)blockIdx.x * 2 * W + c] = v;
     } else {
-      const int col = slot_column<VEC>(c < W ? c : c - W, T);
+      const int col = slot_column<STEP>(c < W ? c : c - W, T);
       float* out = c < W ? a.dgamma : a.dbeta;
       if (out && col < D) out[col] = v;
     }
@@ -359,7 +435,7 @@ __global__ void __launch_bounds__(SMEM_ACC ? 512 : NU > 2 ? 256 : 512, SMEM_ACC 
 // dgamma and dbeta: the blocks' partial sums added per slot. A block of 32
 // slots; thread row j adds the blocks j, j + 32, .. and the 32 sums are added in
 // order.
-template <bool VEC>
+template <int STEP>
 __global__ void __launch_bounds__(1024) layernorm_cols_kernel(const float* partial, int blocks, int D, int W, int T,
                                                               float* dgamma, float* dbeta) {
   __shared__ float part[32][33];
@@ -367,15 +443,17 @@ __global__ void __launch_bounds__(1024) layernorm_cols_kernel(const float* parti
   griddep_wait();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
+  if (c < 2 * W) {
 #pragma unroll 10
-  for (int b = threadIdx.y; b < blocks; b += 32) s += partial[(size_t)b * 2 * W + c];
+    for (int b = threadIdx.y; b < blocks; b += 32) s += partial[(size_t)b * 2 * W + c];
+  }
   part[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.y == 0) {
+  if (threadIdx.y == 0 && c < 2 * W) {
     s = 0.f;
 #pragma unroll
     for (int j = 0; j < 32; ++j) s += part[j][threadIdx.x];
-    const int col = slot_column<VEC>(c < W ? c : c - W, T);
+    const int col = slot_column<STEP>(c < W ? c : c - W, T);
     float* out = c < W ? dgamma : dbeta;
     if (out && col < D) out[col] = s;
   }
@@ -386,42 +464,51 @@ __global__ void __launch_bounds__(1024) layernorm_cols_kernel(const float* parti
 // ---------------------------------------------------------------------------
 typedef void (*LnFn)(const LnArgs);
 
-template <typename TX, typename TY, typename TW, bool VEC>
+template <typename TX, typename TY, typename TW, int STEP>
 LnFn pick_fwd(int NU) {
-  switch (NU) {
-    case 1: return layernorm_kernel<TX, TY, TW, 1, VEC>;
-    case 2: return layernorm_kernel<TX, TY, TW, 2, VEC>;
-    case 3: return layernorm_kernel<TX, TY, TW, 3, VEC>;
-    default: return layernorm_kernel<TX, TY, TW, 4, VEC>;
+  if constexpr (STEP == STEP_T) {
+    return layernorm_kernel<TX, TY, TW, 1, STEP>;
+  } else {
+    switch (NU) {
+      case 1: return layernorm_kernel<TX, TY, TW, 1, STEP>;
+      case 2: return layernorm_kernel<TX, TY, TW, 2, STEP>;
+      case 3: return layernorm_kernel<TX, TY, TW, 3, STEP>;
+      default: return layernorm_kernel<TX, TY, TW, 4, STEP>;
+    }
   }
 }
-template <typename TX, typename TY, typename TW, bool VEC>
+template <typename TX, typename TY, typename TW, int STEP>
 LnFn pick_bwd(int NU, bool smem) {
-  if (smem) return layernorm_bwd_kernel<TX, TY, TW, 4, VEC, true>;
-  switch (NU) {
-    case 1: return layernorm_bwd_kernel<TX, TY, TW, 1, VEC, false>;
-    case 2: return layernorm_bwd_kernel<TX, TY, TW, 2, VEC, false>;
-    case 3: return layernorm_bwd_kernel<TX, TY, TW, 3, VEC, false>;
-    default: return layernorm_bwd_kernel<TX, TY, TW, 4, VEC, false>;
+  if constexpr (STEP == STEP_T) {
+    return layernorm_bwd_kernel<TX, TY, TW, 1, STEP, false>;
+  } else {
+    if (smem) return layernorm_bwd_kernel<TX, TY, TW, 4, STEP, true>;
+    switch (NU) {
+      case 1: return layernorm_bwd_kernel<TX, TY, TW, 1, STEP, false>;
+      case 2: return layernorm_bwd_kernel<TX, TY, TW, 2, STEP, false>;
+      case 3: return layernorm_bwd_kernel<TX, TY, TW, 3, STEP, false>;
+      default: return layernorm_bwd_kernel<TX, TY, TW, 4, STEP, false>;
+    }
   }
 }
 template <typename TX, typename TY, typename TW>
-LnFn pick_v(bool bwd, bool vec, int NU, bool smem) {
-  if (bwd) return vec ? pick_bwd<TX, TY, TW, true>(NU, smem) : pick_bwd<TX, TY, TW, false>(NU, smem);
-  return vec ? pick_fwd<TX, TY, TW, true>(NU) : pick_fwd<TX, TY, TW, false>(NU);
+LnFn pick_v(bool bwd, int step, const LnPlan& p) {
+  if (step == VEC8) return bwd ? pick_bwd<TX, TY, TW, VEC8>(p.NU, p.smem_acc) : pick_fwd<TX, TY, TW, VEC8>(p.NU);
+  if (step == STEP_T) return bwd ? pick_bwd<TX, TY, TW, STEP_T>(p.NU, false) : pick_fwd<TX, TY, TW, STEP_T>(p.NU);
+  return bwd ? pick_bwd<TX, TY, TW, STEP_32>(p.NU, p.smem_acc) : pick_fwd<TX, TY, TW, STEP_32>(p.NU);
 }
-LnFn pick(int xt, int yt, int wt, bool bwd, bool vec, int NU, bool smem) {
+LnFn pick(int xt, int yt, int wt, bool bwd, int step, const LnPlan& p) {
   typedef uint16_t h;
   const int k = (xt == SVLA_TYPE_BF16 ? 4 : 0) | (yt == SVLA_TYPE_BF16 ? 2 : 0) | (wt == SVLA_TYPE_BF16 ? 1 : 0);
   switch (k) {
-    case 0: return pick_v<float, float, float>(bwd, vec, NU, smem);
-    case 1: return pick_v<float, float, h>(bwd, vec, NU, smem);
-    case 2: return pick_v<float, h, float>(bwd, vec, NU, smem);
-    case 3: return pick_v<float, h, h>(bwd, vec, NU, smem);
-    case 4: return pick_v<h, float, float>(bwd, vec, NU, smem);
-    case 5: return pick_v<h, float, h>(bwd, vec, NU, smem);
-    case 6: return pick_v<h, h, float>(bwd, vec, NU, smem);
-    default: return pick_v<h, h, h>(bwd, vec, NU, smem);
+    case 0: return pick_v<float, float, float>(bwd, step, p);
+    case 1: return pick_v<float, float, h>(bwd, step, p);
+    case 2: return pick_v<float, h, float>(bwd, step, p);
+    case 3: return pick_v<float, h, h>(bwd, step, p);
+    case 4: return pick_v<h, float, float>(bwd, step, p);
+    case 5: return pick_v<h, float, h>(bwd, step, p);
+    case 6: return pick_v<h, h, float>(bwd, step, p);
+    default: return pick_v<h, h, h>(bwd, step, p);
   }
 }
 
@@ -465,20 +552,20 @@ bool clash(const Mat& out, const void* v, size_t bytes, int M, int D) {
 }
 
 svla_status run(LnArgs& a, int xt, int yt, int wt, bool bwd, bool vec, cudaStream_t s) {
-  const LnPlan p = ln_plan(a.D, bwd);
+  const LnPlan p = bwd ? ln_bwd_plan(a.D, xt == SVLA_TYPE_BF16 && yt == SVLA_TYPE_BF16) : ln_fwd_plan(a.D, vec, xt == SVLA_TYPE_BF16);
   a.T = p.T;
   a.inv_d = (float)(1.0 / a.D);
-  const bool smem_acc = bwd && a.D > LN_SMEM_ACC_D;
-  const LnFn fn = pick(xt, yt, wt, bwd, vec, p.NU, smem_acc);
+  const int step = vec ? VEC8 : p.T < 32 ? STEP_T : STEP_32;
+  const LnFn fn = pick(xt, yt, wt, bwd, step, p);
   const int blocks = bwd ? ln_bwd_blocks(a.M, p) : (a.M + p.R - 1) / p.R;
   const int W = p.NU * 8 * p.T;
-  const size_t smem = bwd && (smem_acc || a.dgamma || a.dbeta) ? (size_t)(smem_acc ? 1 : p.R) * 2 * W * sizeof(float) : 0;
+  const size_t smem = bwd && (p.smem_acc || a.dgamma || a.dbeta) ? (size_t)(p.smem_acc ? 1 : p.R) * 2 * W * sizeof(float) : 0;
   cudaError_t e = cudaSuccess;
   if (smem > 40 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess) e = launch(fn, dim3(blocks), dim3(p.threads), smem, s, a);
   if (e == cudaSuccess && bwd && blocks > 1 && (a.dgamma || a.dbeta))
-    e = launch(vec ? layernorm_cols_kernel<true> : layernorm_cols_kernel<false>, dim3(2 * W / 32), dim3(32, 32), 0, s,
-               (const float*)a.partial, blocks, a.D, W, p.T, a.dgamma, a.dbeta);
+    e = launch(step == VEC8 ? layernorm_cols_kernel<VEC8> : step == STEP_T ? layernorm_cols_kernel<STEP_T> : layernorm_cols_kernel<STEP_32>,
+               dim3((2 * W + 31) / 32), dim3(32, 32), 0, s, (const float*)a.partial, blocks, a.D, W, p.T, a.dgamma, a.dbeta);
   if (e != cudaSuccess)
     return svla_internal_fail(SVLA_ERR_CUDA, (std::string("layernorm launch: ") + cudaGetErrorString(e)).c_str());
   return SVLA_OK;
@@ -533,9 +620,7 @@ svla_status svla_op_layernorm(const void* x, int x_type, int ldx, const void* ga
 
 size_t svla_op_layernorm_backward_workspace_bytes(int M, int D) {
   if (M < 1 || D < 1 || D > svla::LN_MAX_D) return 0;
-  const svla::LnPlan p = svla::ln_plan(D, true);
-  const int blocks = svla::ln_bwd_blocks(M, p);
-  return blocks > 1 ? (size_t)blocks * 2 * p.NU * 8 * p.T * sizeof(float) : 0;
+  return std::max(svla::ln_bwd_workspace(M, D, true), svla::ln_bwd_workspace(M, D, false));
 }
 
 svla_status svla_op_layernorm_backward(const void* dy, int y_type, int lddy, const void* x, int x_type, int ldx,
