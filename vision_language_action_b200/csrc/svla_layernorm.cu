@@ -19,6 +19,7 @@
 
 #include "common.cuh"
 #include "elements.cuh"
+#include "pairs.cuh"
 
 svla_status svla_internal_fail(svla_status s, const char* msg);
 
@@ -104,16 +105,17 @@ SVLA_DEV int column(int u, int k, int T, int tid) {
   return (u * T + (tid & ~31)) * 8 + k * 32 + (tid & 31);
 }
 
-// one row's elements of this thread as they lie in memory (zeros past the width)
+// One row's elements of this thread (or the weights of its columns) as they lie in
+// memory, from unit u0 on, zeros past the width.
 template <typename E, int NU, int STEP>
 struct RowRegs;
 template <int NU>
 struct RowRegs<float, NU, VEC8> {
   float4 q[2 * NU];
-  SVLA_DEV void load(const float* p, int D, int T, int tid) {
+  SVLA_DEV void load(const float* p, int D, int T, int tid, int u0 = 0) {
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const int c = (u * T + tid) * 8;
+      const int c = ((u0 + u) * T + tid) * 8;
       q[2 * u] = q[2 * u + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c < D) {
         q[2 * u] = *reinterpret_cast<const float4*>(p + c);
@@ -121,54 +123,43 @@ struct RowRegs<float, NU, VEC8> {
       }
     }
   }
-  SVLA_DEV float get(int u, int k) const {
-    const float4& f = q[2 * u + (k >> 2)];
-    return (k & 3) == 0 ? f.x : (k & 3) == 1 ? f.y : (k & 3) == 2 ? f.z : f.w;
+  // elements 2 j and 2 j + 1 of unit u
+  SVLA_DEV f32x2 get2(int u, int j) const {
+    const float4& f = q[2 * u + (j >> 1)];
+    return j & 1 ? pair(f.z, f.w) : pair(f.x, f.y);
   }
 };
 template <int NU>
 struct RowRegs<uint16_t, NU, VEC8> {
   uint4 q[NU];
-  SVLA_DEV void load(const uint16_t* p, int D, int T, int tid) {
+  SVLA_DEV void load(const uint16_t* p, int D, int T, int tid, int u0 = 0) {
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const int c = (u * T + tid) * 8;
+      const int c = ((u0 + u) * T + tid) * 8;
       q[u] = make_uint4(0u, 0u, 0u, 0u);
       if (c < D) q[u] = *reinterpret_cast<const uint4*>(p + c);
     }
   }
-  SVLA_DEV float get(int u, int k) const {
-    const uint32_t w = (k >> 1) == 0 ? q[u].x : (k >> 1) == 1 ? q[u].y : (k >> 1) == 2 ? q[u].z : q[u].w;
-    return __uint_as_float((k & 1) ? (w & 0xffff0000u) : (w << 16));
+  SVLA_DEV f32x2 get2(int u, int j) const {
+    const uint32_t w = j == 0 ? q[u].x : j == 1 ? q[u].y : j == 2 ? q[u].z : q[u].w;
+    return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
 };
 template <typename E, int NU, int STEP>
 struct RowRegs {
   E q[NU * 8];
-  SVLA_DEV void load(const E* p, int D, int T, int tid) {
+  SVLA_DEV void load(const E* p, int D, int T, int tid, int u0 = 0) {
     const int step = STEP == STEP_T ? T : 32;
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const int c = column<STEP>(u, 0, T, tid);
+      const int c = column<STEP>(u0 + u, 0, T, tid);
 #pragma unroll
       for (int k = 0; k < 8; ++k) q[u * 8 + k] = c + k * step < D ? p[c + k * step] : E(0);
     }
   }
-  SVLA_DEV float get(int u, int k) const { return load1(&q[u * 8 + k]); }
+  SVLA_DEV f32x2 get2(int u, int j) const { return pair(load1(&q[u * 8 + 2 * j]), load1(&q[u * 8 + 2 * j + 1])); }
 };
 
-// columns of a vector of weights into 8 floats of unit u
-template <typename TW, int STEP>
-SVLA_DEV void load_unit(const TW* w, int u, int D, int T, int tid, float (&x)[8]) {
-  const int c = column<STEP>(u, 0, T, tid);
-  if constexpr (STEP == VEC8) {
-    if (c < D) load8(w + c, x);
-  } else {
-    const int step = STEP == STEP_T ? T : 32;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = c + k * step < D ? load1(w + c + k * step) : 0.f;
-  }
-}
 template <typename E, int STEP>
 SVLA_DEV void store_unit(E* p, int u, int D, int T, int tid, const float (&x)[8]) {
   const int c = column<STEP>(u, 0, T, tid);
@@ -258,22 +249,29 @@ __global__ void __launch_bounds__(NU <= 2 ? 1024 : 256) layernorm_kernel(const L
     cnt = (float)mine;
     inv_cnt = mine ? 1.f / cnt : 0.f;
   }
-  float s = 0.f;
+  f32x2 s2 = both(0.f);
 #pragma unroll
   for (int u = 0; u < NU; ++u)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += x.get(u, k);
+    for (int j = 0; j < 4; ++j) s2 = add2(s2, x.get2(u, j));
+  float s = halves(s2).x + halves(s2).y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     if (o < width) s += __shfl_xor_sync(0xffffffffu, s, o);
-  float mean = s * inv_cnt, m2 = 0.f;
+  float mean = s * inv_cnt;
+  s2 = both(0.f);
 #pragma unroll
   for (int u = 0; u < NU; ++u)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float d = x.get(u, k) - mean;
-      if (column<STEP>(u, k, T, tid) < D) m2 = fmaf(d, d, m2);
+    for (int j = 0; j < 4; ++j) {
+      f32x2 d = add2(x.get2(u, j), both(-mean));
+      if (STEP != VEC8) {
+        const float2 h = halves(d);
+        d = pair(column<STEP>(u, 2 * j, T, tid) < D ? h.x : 0.f, column<STEP>(u, 2 * j + 1, T, tid) < D ? h.y : 0.f);
+      }
+      if (STEP != VEC8 || column<STEP>(u, 0, T, tid) < D) s2 = fma2(d, d, s2);
     }
+  float m2 = halves(s2).x + halves(s2).y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     if (o < width) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
@@ -291,11 +289,16 @@ __global__ void __launch_bounds__(NU <= 2 ? 1024 : 256) layernorm_kernel(const L
   TY* y = reinterpret_cast<TY*>(a.out) + row * a.ldo;
 #pragma unroll
   for (int u = 0; u < NU; ++u) {
-    float g[8], b[8] = {}, o[8];
-    load_unit<TW, STEP>(reinterpret_cast<const TW*>(a.gamma), u, D, T, tid, g);
-    if (a.beta) load_unit<TW, STEP>(reinterpret_cast<const TW*>(a.beta), u, D, T, tid, b);
+    RowRegs<TW, 1, STEP> g, b;
+    g.load(reinterpret_cast<const TW*>(a.gamma), D, T, tid, u);
+    b.load(reinterpret_cast<const TW*>(a.beta ? a.beta : a.gamma), a.beta ? D : 0, T, tid, u);
+    float o[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = fmaf((x.get(u, k) - mean) * rstd, g[k], b[k]);
+    for (int j = 0; j < 4; ++j) {
+      const float2 h = halves(fma2(mul2(add2(x.get2(u, j), both(-mean)), both(rstd)), g.get2(0, j), b.get2(0, j)));
+      o[2 * j] = h.x;
+      o[2 * j + 1] = h.y;
+    }
     store_unit<TY, STEP>(y, u, D, T, tid, o);
   }
   if (tid == 0) {
@@ -332,13 +335,17 @@ __global__ void __launch_bounds__(STEP == STEP_T ? 256 : 512)
   const int W = NU * 8 * T;  // slots
   const TX* xp = reinterpret_cast<const TX*>(a.x);
   const TY* dyp = reinterpret_cast<const TY*>(a.dy);
-  float ag[SMEM_ACC ? 1 : NU * 8], ab[SMEM_ACC ? 1 : NU * 8];
+  f32x2 ag[SMEM_ACC ? 1 : NU * 4], ab[SMEM_ACC ? 1 : NU * 4];
+  // the weights stay in registers where they take no more than 16
+  constexpr bool KEEP = NU * 2 * sizeof(TW) <= 16;
+  RowRegs<TW, KEEP ? NU : 1, STEP> g;
+  if (KEEP) g.load(reinterpret_cast<const TW*>(a.gamma), D, T, tid);
   if constexpr (SMEM_ACC) {
     for (int c = threadIdx.x; c < 2 * W; c += blockDim.x) cols[c] = 0.f;
     __syncthreads();
   } else {
 #pragma unroll
-    for (int j = 0; j < NU * 8; ++j) ag[j] = ab[j] = 0.f;
+    for (int j = 0; j < NU * 4; ++j) ag[j] = ab[j] = both(0.f);
   }
   const long long stride = (long long)gridDim.x * R;
   long long row0 = (long long)blockIdx.x * R;
@@ -364,26 +371,29 @@ __global__ void __launch_bounds__(STEP == STEP_T ? 256 : 512)
     } else {
       fetch(row, x, dy, mean, rstd);
     }
-    float s0 = 0.f, s1 = 0.f;  // sums of w and of w xh
+    f32x2 w2 = both(0.f), x2 = both(0.f);  // sums of w and of w xh
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      float g[8] = {};
-      load_unit<TW, STEP>(reinterpret_cast<const TW*>(a.gamma), u, D, T, tid, g);
+      if (!KEEP) g.load(reinterpret_cast<const TW*>(a.gamma), D, T, tid, u);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float d = dy.get(u, k), xh = (x.get(u, k) - mean) * rstd, w = d * g[k];
-        s0 += w;
-        s1 = fmaf(w, xh, s1);
+      for (int j = 0; j < 4; ++j) {
+        const f32x2 d = dy.get2(u, j), xh = mul2(add2(x.get2(u, j), both(-mean)), both(rstd)), w = mul2(d, g.get2(KEEP ? u : 0, j));
+        w2 = add2(w2, w);
+        x2 = fma2(w, xh, x2);
         if constexpr (SMEM_ACC) {
-          float* c = cols + (u * 8 + k) * T + tid;
-          c[0] = fmaf(d, xh, c[0]);
-          c[W] += d;
+          const float2 dh = halves(d), xx = halves(xh);
+          float* c = cols + (u * 8 + 2 * j) * T + tid;
+          c[0] = fmaf(dh.x, xx.x, c[0]);
+          c[T] = fmaf(dh.y, xx.y, c[T]);
+          c[W] += dh.x;
+          c[W + T] += dh.y;
         } else {
-          ag[u * 8 + k] = fmaf(d, xh, ag[u * 8 + k]);
-          ab[u * 8 + k] += d;
+          ag[u * 4 + j] = fma2(d, xh, ag[u * 4 + j]);
+          ab[u * 4 + j] = add2(ab[u * 4 + j], d);
         }
       }
     }
+    float s0 = halves(w2).x + halves(w2).y, s1 = halves(x2).x + halves(x2).y;
     row_sums(s0, s1, T, red[it & 1]);
     s0 *= a.inv_d;
     s1 *= a.inv_d;
@@ -391,12 +401,14 @@ __global__ void __launch_bounds__(STEP == STEP_T ? 256 : 512)
       TX* dx = reinterpret_cast<TX*>(a.out) + row * a.ldo;
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
-        float g[8] = {}, o[8];
-        load_unit<TW, STEP>(reinterpret_cast<const TW*>(a.gamma), u, D, T, tid, g);
+        if (!KEEP) g.load(reinterpret_cast<const TW*>(a.gamma), D, T, tid, u);
+        float o[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float xh = (x.get(u, k) - mean) * rstd, w = dy.get(u, k) * g[k];
-          o[k] = rstd * (w - s0 - xh * s1);
+        for (int j = 0; j < 4; ++j) {
+          const f32x2 xh = mul2(add2(x.get2(u, j), both(-mean)), both(rstd)), w = mul2(dy.get2(u, j), g.get2(KEEP ? u : 0, j));
+          const float2 h = halves(mul2(add2(fma2(xh, both(-s1), w), both(-s0)), both(rstd)));
+          o[2 * j] = h.x;
+          o[2 * j + 1] = h.y;
         }
         store_unit<TX, STEP>(dx, u, D, T, tid, o);
       }
@@ -412,9 +424,11 @@ __global__ void __launch_bounds__(STEP == STEP_T ? 256 : 512)
   if constexpr (!SMEM_ACC) {
     float* mine = cols + (size_t)group * 2 * W + tid;
 #pragma unroll
-    for (int j = 0; j < NU * 8; ++j) {
-      mine[j * T] = ag[j];
-      mine[W + j * T] = ab[j];
+    for (int j = 0; j < NU * 4; ++j) {
+      mine[2 * j * T] = halves(ag[j]).x;
+      mine[(2 * j + 1) * T] = halves(ag[j]).y;
+      mine[W + 2 * j * T] = halves(ab[j]).x;
+      mine[W + (2 * j + 1) * T] = halves(ab[j]).y;
     }
   }
   __syncthreads();
