@@ -445,8 +445,8 @@ SVLA_API svla_status svla_op_rmsnorm(const float* x, const void* g, int M, int D
  *   mean, rstd: device float32 [M], written by the forward (each may be NULL
  *     there) and read by the backward.
  *   dgamma, dbeta: device float32 [D], written in full (not added to), each
- *     NULL to leave out. Their sums run in an order that M and D fix: results
- *     are bitwise reproducible.
+ *     NULL to leave out. Their sums run in an order that the sizes, types and
+ *     alignment fix: results are bitwise reproducible.
  *   y may be x itself and dx may be x or dy itself (same pointer, type and
  *     stride); any other overlap of an output with another argument is
  *     SVLA_ERR_ARG.

@@ -13,6 +13,7 @@
 // 32-byte accesses); else (an odd width, stride or address) every 32nd (narrow:
 // T-th) one.
 #include <algorithm>
+#include <atomic>
 #include <exception>
 #include <string>
 #include <utility>
@@ -27,7 +28,8 @@ namespace svla {
 namespace {
 
 constexpr int LN_MAX_D = 16384;
-constexpr int LN_BWD_BLOCKS = 296;  // blocks (partial sums of dgamma and dbeta): 2 on each of 148 SMs
+constexpr int LN_SMS = 148;
+constexpr int LN_BWD_PER_SM = 4;  // blocks an SM at most (each has partial sums of dgamma and dbeta)
 
 struct LnPlan {
   int T, NU, R, threads;  // threads a row, units a thread, rows a block, threads a block
@@ -56,26 +58,26 @@ LnPlan ln_plan(int D, int max_nu, int max_t) {
   p.threads = p.R * p.T;
   return p;
 }
-// Forward: one warp a row up to 1024 columns, then two units a thread (up to 1024 threads a row). Rows of bf16 without
-// the wide accesses are bound by the number of 2-byte accesses in flight: one unit a thread from 257 columns up (30000
-// rows of 1283: 81 us, 116 with two; fp32 rows 79 with one, 69 with two).
+// Forward: one warp a row up to 1024 columns, then four units a thread: the fewer threads share a row, the more rows
+// are on their way at once (4000 bf16 rows of 12288: 58 us with four units, 94 with two; 16384 of 4096: 62 and 73).
+// Without the wide accesses two (fp32) or, from 257 columns up, one (bf16: the number of 2-byte accesses in flight bounds
+// those; 30000 rows of 1283: 79 us, 116 with two).
 LnPlan ln_fwd_plan(int D, bool vec, bool bf16_x) {
   if (!vec && bf16_x && D > 256) return ln_plan(D, D <= 8192 ? 1 : 2, 1024);
-  return D <= 1024 ? ln_plan(D, 4, 32) : ln_plan(D, 2, 1024);
+  return ln_plan(D, vec || D <= 1024 ? 4 : 2, 1024);
 }
-// Backward: 16 sums and, per unit, 4 (bf16) or 8 (fp32) registers of x and of dy, beside the rest in the 128
-// registers of 512 threads an SM. One warp a row up to 1024 columns; two units a thread while 512 threads hold the
-// row so (the next row's registers fit beside it); then three or, of bf16 rows, four. What is wider keeps its columns'
-// sums in shared memory.
-LnPlan ln_bwd_plan(int D, bool bf16_rows) {
-  if (D <= 1024) return ln_plan(D, 4, 32);
-  return ln_plan(D, D <= 8192 ? 2 : D <= 12288 ? 3 : bf16_rows ? 4 : 3, 512);
-}
+// Backward: 16 sums and, per unit, 4 (bf16) or 8 (fp32) registers of x and of dy have to fit beside the rest in the 128
+// registers of 512 threads an SM. One warp a row up to 768 columns (three units a thread); then two units while 512
+// threads hold the row so (the next row's registers fit beside it: 16384 bf16 rows of 4096 in 81 us; three units 94),
+// then three. What is wider than 12288 keeps its columns' sums in shared memory.
+LnPlan ln_bwd_plan(int D) { return D <= 768 ? ln_plan(D, 3, 32) : ln_plan(D, D <= 8192 ? 2 : 3, 512); }
 
-int ln_bwd_blocks(int M, const LnPlan& p) { return std::min((M + p.R - 1) / p.R, LN_BWD_BLOCKS); }
-size_t ln_bwd_workspace(int M, int D, bool bf16_rows) {
-  const LnPlan p = ln_bwd_plan(D, bf16_rows);
-  const int blocks = ln_bwd_blocks(M, p);
+int ln_bwd_blocks(int M, const LnPlan& p, int per_sm) {
+  return std::min((M + p.R - 1) / p.R, LN_SMS * std::min(per_sm, LN_BWD_PER_SM));
+}
+size_t ln_bwd_workspace(int M, int D) {
+  const LnPlan p = ln_bwd_plan(D);
+  const int blocks = ln_bwd_blocks(M, p, LN_BWD_PER_SM);
   return blocks > 1 ? (size_t)blocks * 2 * p.NU * 8 * p.T * sizeof(float) : 0;
 }
 
@@ -230,15 +232,12 @@ struct Moments {
 // barrier a row.
 // ---------------------------------------------------------------------------
 template <typename TX, typename TY, typename TW, int NU, int STEP>
-__global__ void __launch_bounds__(NU <= 2 ? 1024 : 256) layernorm_kernel(const LnArgs a) {
+__global__ void __launch_bounds__(NU <= 2 ? 1024 : 512) layernorm_kernel(const LnArgs a) {
   __shared__ Moments red[32];
   griddep_launch_dependents();
   griddep_wait();  // nothing is read before: the weights may come from an optimiser step
   const int T = a.T, tid = threadIdx.x % T, D = a.D;
   const long long row = (long long)blockIdx.x * (blockDim.x / T) + threadIdx.x / T;
-  const bool active = row < a.M;
-  RowRegs<TX, NU, STEP> x;
-  x.load(reinterpret_cast<const TX*>(a.x) + (active ? row : 0) * a.ldx, D, T, tid);
   // columns of this thread's warp (or part of one): whole units of 256, the last one cut
   const int width = min(T, 32);
   float cnt = (float)D, inv_cnt = a.inv_d;
@@ -249,6 +248,9 @@ __global__ void __launch_bounds__(NU <= 2 ? 1024 : 256) layernorm_kernel(const L
     cnt = (float)mine;
     inv_cnt = mine ? 1.f / cnt : 0.f;
   }
+  const bool active = row < a.M;
+  RowRegs<TX, NU, STEP> x;
+  x.load(reinterpret_cast<const TX*>(a.x) + (active ? row : 0) * a.ldx, D, T, tid);
   f32x2 s2 = both(0.f);
 #pragma unroll
   for (int u = 0; u < NU; ++u)
@@ -500,8 +502,7 @@ LnFn pick_bwd(int NU, bool smem) {
     switch (NU) {
       case 1: return layernorm_bwd_kernel<TX, TY, TW, 1, STEP, false>;
       case 2: return layernorm_bwd_kernel<TX, TY, TW, 2, STEP, false>;
-      case 3: return layernorm_bwd_kernel<TX, TY, TW, 3, STEP, false>;
-      default: return layernorm_bwd_kernel<TX, TY, TW, 4, STEP, false>;
+      default: return layernorm_bwd_kernel<TX, TY, TW, 3, STEP, false>;
     }
   }
 }
@@ -565,17 +566,35 @@ bool clash(const Mat& out, const void* v, size_t bytes, int M, int D) {
   return v && overlap(out.begin(), out.end(M, D), (uintptr_t)v, (uintptr_t)v + bytes);
 }
 
+// Blocks of a kernel that an SM holds, asked for once a kernel: the backward's rows are walked by what is resident.
+cudaError_t resident_per_sm(LnFn fn, int slot, int threads, size_t smem, int* blocks) {
+  static std::atomic<int> known[8 * 3 * 17 * 4];  // by types, way of access, threads a row and units a thread
+  if ((*blocks = known[slot].load()) != 0) return cudaSuccess;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, fn, threads, smem);
+  if (e != cudaSuccess) return e;
+  if (*blocks < 1) return cudaErrorInvalidConfiguration;
+  known[slot].store(*blocks);
+  return cudaSuccess;
+}
+
 svla_status run(LnArgs& a, int xt, int yt, int wt, bool bwd, bool vec, cudaStream_t s) {
-  const LnPlan p = bwd ? ln_bwd_plan(a.D, xt == SVLA_TYPE_BF16 && yt == SVLA_TYPE_BF16) : ln_fwd_plan(a.D, vec, xt == SVLA_TYPE_BF16);
+  const LnPlan p = bwd ? ln_bwd_plan(a.D) : ln_fwd_plan(a.D, vec, xt == SVLA_TYPE_BF16);
   a.T = p.T;
   a.inv_d = (float)(1.0 / a.D);
   const int step = vec ? VEC8 : p.T < 32 ? STEP_T : STEP_32;
   const LnFn fn = pick(xt, yt, wt, bwd, step, p);
-  const int blocks = bwd ? ln_bwd_blocks(a.M, p) : (a.M + p.R - 1) / p.R;
   const int W = p.NU * 8 * p.T;
-  const size_t smem = bwd && (p.smem_acc || a.dgamma || a.dbeta) ? (size_t)(p.smem_acc ? 1 : p.R) * 2 * W * sizeof(float) : 0;
+  const size_t full = bwd ? (size_t)(p.smem_acc ? 1 : p.R) * 2 * W * sizeof(float) : 0;
+  const size_t smem = p.smem_acc || a.dgamma || a.dbeta ? full : 0;
+  int blocks = (a.M + p.R - 1) / p.R;
   cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (full > 40 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)full);
+  if (e == cudaSuccess && bwd && blocks > 1) {
+    int per_sm = 0;
+    const int kind = (xt == SVLA_TYPE_BF16 ? 4 : 0) | (yt == SVLA_TYPE_BF16 ? 2 : 0) | (wt == SVLA_TYPE_BF16 ? 1 : 0);
+    e = resident_per_sm(fn, ((kind * 3 + step) * 17 + p.T / 32) * 4 + p.NU - 1, p.threads, full, &per_sm);
+    if (e == cudaSuccess) blocks = ln_bwd_blocks(a.M, p, per_sm);
+  }
   if (e == cudaSuccess) e = launch(fn, dim3(blocks), dim3(p.threads), smem, s, a);
   if (e == cudaSuccess && bwd && blocks > 1 && (a.dgamma || a.dbeta))
     e = launch(step == VEC8 ? layernorm_cols_kernel<VEC8> : step == STEP_T ? layernorm_cols_kernel<STEP_T> : layernorm_cols_kernel<STEP_32>,
@@ -634,7 +653,7 @@ svla_status svla_op_layernorm(const void* x, int x_type, int ldx, const void* ga
 
 size_t svla_op_layernorm_backward_workspace_bytes(int M, int D) {
   if (M < 1 || D < 1 || D > svla::LN_MAX_D) return 0;
-  return std::max(svla::ln_bwd_workspace(M, D, true), svla::ln_bwd_workspace(M, D, false));
+  return svla::ln_bwd_workspace(M, D);
 }
 
 svla_status svla_op_layernorm_backward(const void* dy, int y_type, int lddy, const void* x, int x_type, int ldx,
