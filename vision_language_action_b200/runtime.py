@@ -233,18 +233,19 @@ class SmolVLA:
         ``new_moments``, ``step`` counts from 1, ``max_norm`` > 0 clips by the global norm (into ``grad_norm``)."""
         m, v, ms, vs = moments
         n, k = int(self.lib.svla_train_grad_elems(self.h)), int(self.lib.svla_train_scale_elems(self.h))
-        bits = 32 if m.dtype == torch.float32 else 8
+        dev, f32 = self.device, torch.float32
+        bits = 32 if m.dtype == f32 else 8
         kinds = (torch.float32, torch.float32) if bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
         a = _abi.SvlaAdamwArgs()
         a.param_type = a.grad_type = _abi.TYPE_F32
         a.state_bits, a.lr, (a.beta1, a.beta2), a.eps = bits, lr, betas, eps
         a.weight_decay, a.max_norm, a.step, a.seed = weight_decay, max_norm, step, seed
         st = self.lib.svla_train_update(
-            self.h, _vec(master, n, "master", torch.float32), _vec(grads, n, "grads", torch.float32),
-            _vec(m, n, "m", kinds[0]), _vec(v, n, "v", kinds[1]),
-            _vec(ms, k, "m_scale", torch.float32) if bits == 8 else None,
-            _vec(vs, k, "v_scale", torch.float32) if bits == 8 else None, ctypes.byref(a),
-            _vec(grad_norm, 1, "grad_norm", torch.float32), _stream(stream))
+            self.h, _vec(master, n, "master", f32, dev), _vec(grads, n, "grads", f32, dev),
+            _vec(m, n, "m", kinds[0], dev), _vec(v, n, "v", kinds[1], dev),
+            _vec(ms, k, "m_scale", f32, dev) if bits == 8 else None,
+            _vec(vs, k, "v_scale", f32, dev) if bits == 8 else None, ctypes.byref(a),
+            _vec(grad_norm, 1, "grad_norm", f32, dev), _stream(stream))
         _abi.check(st, self.h)
 
     def set_prefix_weights(self, bits: int) -> None:
@@ -350,9 +351,9 @@ def _type(t: torch.Tensor, what: str) -> int:
     return kind
 
 
-def _rows(t: torch.Tensor, M: int, D: int, device, what: str):
-    """(address, type, row stride) of a [M, D] CUDA matrix whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != D or t.device != device or not t.is_cuda:
+def _rows(t: torch.Tensor, M: int, D: int, dev: int, what: str):
+    """(address, type, row stride) of a [M, D] matrix on device `dev` whose rows are contiguous."""
+    if t.get_device() != dev or dev < 0 or t.dim() != 2 or t.shape[0] != M or t.shape[1] != D:
         raise ValueError(f"{what}: a CUDA matrix of shape {(M, D)} on x's device expected")
     ld, one = t.stride()
     if M <= 1:
@@ -362,26 +363,23 @@ def _rows(t: torch.Tensor, M: int, D: int, device, what: str):
     return t.data_ptr(), _type(t, what), ld
 
 
-def _vec(t: Optional[torch.Tensor], n: int, what: str, dtype: Optional[torch.dtype] = None, device=None):
+def _vec(t: Optional[torch.Tensor], n: int, what: str, dtype: Optional[torch.dtype], dev: int):
+    """Address of a contiguous tensor of n elements on device `dev` (None for None; dtype None: any)."""
     if t is None:
         return None
-    if not t.is_cuda or not t.is_contiguous() or t.numel() != n or (dtype is not None and t.dtype != dtype) or (
-            device is not None and t.device != device):
-        raise ValueError(f"{what}: a contiguous CUDA tensor of {n} {dtype or 'float32 or bfloat16'} elements"
-                         f"{'' if device is None else f' on {device}'} expected")
+    if t.get_device() != dev or dev < 0 or t.numel() != n or (dtype is not None and t.dtype != dtype) or \
+            not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous tensor of {n} {dtype or 'float32 or bfloat16'} elements on "
+                         f"cuda:{dev} expected")
     return t.data_ptr()
 
 
-def _launch(device, stream, fn, *args) -> int:
-    """fn(*args, stream) with `device` current, on `stream` or on the device's current one."""
-    if stream is not None:
-        raw = stream.cuda_stream
-    else:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
-        return fn(*args, raw)
-    with torch.cuda.device(device):
-        return fn(*args, raw)
+def _launch(dev: int, stream, fn, *args) -> int:
+    """fn(*args, stream) with device `dev` current, on `stream` or on the device's current one."""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _launch(dev, stream, fn, *args)
+    return fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
 
 
 def _scratch(nbytes: int, device, stream) -> Optional[torch.Tensor]:
@@ -402,7 +400,7 @@ def op_layernorm(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tens
     lib = _abi.load()
     if x.dim() != 2:
         raise ValueError("x: a [M, D] matrix expected")
-    (M, D), dev, f32 = x.shape, x.device, torch.float32
+    (M, D), dev, f32 = x.shape, x.get_device(), torch.float32
     px, tx, ldx = _rows(x, M, D, dev, "x")
     py, ty, ldy = _rows(y, M, D, dev, "y")
     st = _launch(dev, stream, lib.svla_op_layernorm, px, tx, ldx, _vec(gamma, D, "gamma", None, dev),
@@ -420,7 +418,7 @@ def op_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor
     lib = _abi.load()
     if x.dim() != 2:
         raise ValueError("x: a [M, D] matrix expected")
-    (M, D), dev, f32 = x.shape, x.device, torch.float32
+    (M, D), dev, f32 = x.shape, x.get_device(), torch.float32
     px, tx, ldx = _rows(x, M, D, dev, "x")
     pdy, ty, lddy = _rows(dy, M, D, dev, "dy")
     pdx, tdx, lddx = _rows(dx, M, D, dev, "dx")
@@ -429,7 +427,7 @@ def op_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor
     n = 0
     if dgamma is not None or dbeta is not None:
         n = lib.svla_op_layernorm_backward_workspace_bytes(M, D)
-    ws = _scratch(n, dev, stream)
+    ws = _scratch(n, x.device, stream)
     st = _launch(dev, stream, lib.svla_op_layernorm_backward, pdy, ty, lddy, px, tx, ldx,
                  _vec(gamma, D, "gamma", None, dev), _type(gamma, "gamma"), _vec(mean, M, "mean", f32, dev),
                  _vec(rstd, M, "rstd", f32, dev), M, D, pdx, lddx, _vec(dgamma, D, "dgamma", f32, dev),
@@ -456,57 +454,46 @@ class AdamW:
                  eps: float = 1e-8, weight_decay: float = 1e-2, state_bits: int = 32, max_norm: float = 0.0,
                  copies: Optional[Sequence[Optional[torch.Tensor]]] = None, decay: Optional[Sequence[bool]] = None,
                  seed: int = 0, step: int = 0, state=None, capturable: bool = False):
+        import numpy as np
         self.lib = _abi.load()
         self.params: List[torch.Tensor] = list(params)
         n = len(self.params)
         if n == 0:
             raise ValueError("no parameters")
-        dev, dt = self.params[0].device, self.params[0].dtype
-        for p in self.params:
-            if not p.is_cuda or p.device != dev or p.dtype != dt or not p.is_contiguous():
-                raise ValueError("parameters: contiguous CUDA tensors of one type on one device expected")
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
+        if step < 0:
+            raise ValueError("step: the number of steps taken")
+        dev, size = self.params[0].device, [p.numel() for p in self.params]
+        self._check(self.params, size, self.params[0].dtype, self.params[0].get_device(), "parameters")
         self.device, self.state_bits, self.lr, self.steps = dev, state_bits, lr, int(step)
-        size = [p.numel() for p in self.params]
+        self._dev = self.params[0].get_device()
+        per = [(k + 255) // 256 for k in size]
+        kinds = (torch.float32, torch.float32) if state_bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
         if state is None:
             # one buffer a moment; every tensor's part starts at a multiple of 8 elements
-            unit = 8
             at = [0]
             for k in size:
-                at.append(at[-1] + (k + unit - 1) // unit * unit)
-            kinds = ((torch.float32,) * 2) if state_bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
-            flat = [torch.zeros(at[-1] * (4 if state_bits == 32 else 1), dtype=torch.uint8, device=dev).view(k)
-                    for k in kinds]
-            self.m, self.v = ([f[a:a + k] for a, k in zip(at, size)] for f in flat)
-            self.m_scale = self.v_scale = None
-            if state_bits == 8:
-                per = [(k + 255) // 256 for k in size]
-                self.m_scale = list(torch.zeros(sum(per), device=dev).split(per))
-                self.v_scale = list(torch.zeros(sum(per), device=dev).split(per))
-        else:
-            self.m, self.v, self.m_scale, self.v_scale = (None if x is None else list(x) for x in state)
-            kinds = ((torch.float32,) * 2) if state_bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
-            for i, k in enumerate(size):
-                for what, x, d, c in (("m", self.m[i], kinds[0], k), ("v", self.v[i], kinds[1], k)) + (
-                        () if state_bits == 32 else (("m_scale", self.m_scale[i], torch.float32, (k + 255) // 256),
-                                                     ("v_scale", self.v_scale[i], torch.float32, (k + 255) // 256))):
-                    _vec(x, c, f"{what} of parameter {i}", d, dev)
+                at.append(at[-1] + (k + 7) // 8 * 8)
+            flat = [torch.zeros(at[-1] * (state_bits // 8), dtype=torch.uint8, device=dev).view(k) for k in kinds]
+            state = [[f[a:a + k] for a, k in zip(at, size)] for f in flat]
+            state += [None, None] if state_bits == 32 else [torch.zeros(sum(per), device=dev).split(per) for _ in "mv"]
+        self.m, self.v, self.m_scale, self.v_scale = (None if x is None else list(x) for x in state)
         self.copies = [None] * n if copies is None else list(copies)
         flags = [True] * n if decay is None else [bool(d) for d in decay]
-        if len(self.copies) != n or len(flags) != n or len(self.m) != n or len(self.v) != n:
-            raise ValueError("copies, decay and state must have one entry a parameter")
-        self._size = size
+        if len(flags) != n:
+            raise ValueError("decay must have one entry a parameter")
         # the C table, as an array whose columns are filled at once
-        import numpy as np
-        self._table = np.zeros(n, dtype=np.dtype(_abi.SvlaAdamwTensor))
+        self._size, self._table = size, np.zeros(n, dtype=np.dtype(_abi.SvlaAdamwTensor))
         self._table_ptr = ctypes.cast(self._table.ctypes.data, ctypes.POINTER(_abi.SvlaAdamwTensor))
-        address = lambda ts: [0 if t is None else t.data_ptr() for t in ts]
-        for i, t in enumerate(self.copies):
-            _vec(t, size[i], f"copy of parameter {i}", torch.bfloat16, dev)
-        for column, ts in (("param", self.params), ("m", self.m), ("v", self.v), ("copy", self.copies)) + (
-                () if state_bits == 32 else (("m_scale", self.m_scale), ("v_scale", self.v_scale))):
-            self._table[column] = address(ts)
+        columns = [("param", self.params, size, self.params[0].dtype), ("m", self.m, size, kinds[0]),
+                   ("v", self.v, size, kinds[1]), ("copy", self.copies, size, torch.bfloat16)]
+        if state_bits == 8:
+            columns += [("m_scale", self.m_scale, per, torch.float32), ("v_scale", self.v_scale, per, torch.float32)]
+        for column, ts, sizes, kind in columns:
+            if column != "param":
+                self._check(ts, sizes, kind, self._dev, column, column == "copy")
+            self._table[column] = [0 if t is None else t.data_ptr() for t in ts]
         self._table["n"], self._table["decay"] = size, flags
         self.capturable = capturable
         self.step_tensor = torch.full((1,), self.steps, dtype=torch.int64, device=dev) if capturable else None
@@ -523,18 +510,27 @@ class AdamW:
         self._ws_ptr = self._ws.data_ptr() if ws else None
         self._norm_ptr = self.grad_norm.data_ptr() if max_norm else None
 
+    @staticmethod
+    def _check(ts, sizes, dtype, dev: int, what: str, none_too: bool = False) -> None:
+        if ts is None or len(ts) != len(sizes):
+            raise ValueError(f"{what}: one tensor a parameter expected")
+        for i, (t, k) in enumerate(zip(ts, sizes)):
+            if t is None and none_too:
+                continue
+            if t is None or t.dtype != dtype or t.get_device() != dev or dev < 0 or t.numel() != k or \
+                    not t.is_contiguous():
+                raise ValueError(f"{what} of parameter {i}: a contiguous tensor of {k} {dtype} elements on "
+                                 f"cuda:{dev} expected")
+
     def _check_lr(self, lr: torch.Tensor) -> None:
         if not self.capturable or lr.dtype != torch.float64 or lr.device != self.device or lr.numel() != 1:
             raise ValueError("a tensor lr: one float64 on the parameters' device, with capturable")
 
     def step(self, grads: Sequence[torch.Tensor], lr: Optional[float] = None, stream=None) -> None:
         """One step with these gradients (float32 or bfloat16, all one type, one contiguous tensor a parameter)."""
-        if len(grads) != len(self._size):
-            raise ValueError(f"{len(self._size)} gradients expected, got {len(grads)}")
-        dt, dev = grads[0].dtype, self.device
-        for g, k in zip(grads, self._size):
-            if g.dtype != dt or g.device != dev or g.numel() != k or not g.is_contiguous():
-                raise ValueError("gradients: contiguous tensors of one type and the parameters' sizes, on their device")
+        if len(grads) == 0:
+            raise ValueError("no gradients")
+        self._check(grads, self._size, grads[0].dtype, self._dev, "gradients")
         self._table["grad"] = [g.data_ptr() for g in grads]
         a = self._args
         a.grad_type = _type(grads[0], "gradients")
@@ -546,10 +542,10 @@ class AdamW:
         else:
             a.lr, a.lr_device = rate, None
         if self.capturable:
-            on = stream if stream is not None else torch.cuda.current_stream(dev)
+            on = stream if stream is not None else torch.cuda.current_stream(self.device)
             with torch.cuda.stream(on):
                 self.step_tensor.add_(1)
-        st = _launch(dev, stream, self.lib.svla_op_adamw, self._table_ptr, len(self._size), self._args_ref, self._ws_ptr,
+        st = _launch(self._dev, stream, self.lib.svla_op_adamw, self._table_ptr, len(self._size), self._args_ref, self._ws_ptr,
                      self._ws_bytes, self._norm_ptr)
         if st:
             if self.capturable:
