@@ -439,6 +439,7 @@ SVLA_API svla_status svla_op_rmsnorm(const float* x, const void* g, int M, int D
  *   backward, xh = (x - mu) r, w = dy gamma:
  *     dx = r (w - mean(w) - xh mean(w xh)), dgamma = sum dy xh, dbeta = sum dy
  * Statistics and sums are fp32; y and dx are rounded once, to nearest even.
+ *   Pointers are of the current device.
  *   x, dy, y, dx: device, SVLA_TYPE_F32 or SVLA_TYPE_BF16 each (dy has y's
  *     type, dx has x's), row strides in elements, >= D, of any alignment.
  *   gamma, beta: device, w_type [D]; beta NULL: 0.
@@ -477,7 +478,8 @@ SVLA_API size_t svla_op_layernorm_backward_workspace_bytes(int M, int D);
  * finite the step is skipped: nothing but grad_norm is written. max_norm =
  * INFINITY measures G and skips, without clipping. With max_norm = 0 c is 1,
  * grad_norm is not written, and a gradient that is not finite makes its
- * element's parameter and moments NaN.
+ * element's parameter and moments NaN. (fp32 ends here: a |g'| from 1.8e19 up
+ * makes v infinite and the element's step 0.)
  * state_bits 32: m and v are float32 [n].
  * state_bits 8: m holds e4m3 codes and v e5m2 codes (uint8 [n]), m_scale and
  *   v_scale a float32 for every 256 consecutive elements of the tensor
@@ -485,19 +487,21 @@ SVLA_API size_t svla_op_layernorm_backward_workspace_bytes(int M, int D);
  *   puts the largest magnitude of its 256 into [2^7, 2^8) (m) or [2^14, 2^15)
  *   (v); 0 where all are 0. Magnitudes are rounded up with the probability of
  *   their distance to the lower code, from 16 random bits: Philox4x32-10 with
- *   key = seed, counter {k / 8 low, k / 8 high, t, tensor index} for element k,
+ *   key = seed, counter {k / 8 low, k / 8 high, t low, tensor index} for element k,
  *   half k % 8 of the 128 bits (low half of a word first). No subnormal codes:
  *   an m then below 2^-6 of its scale becomes 0, a v > 0 is at least 2^-14 of it.
- *   Zero bytes are a valid start (all moments 0).
- * The device pointers and n of all tensors; the table is read during the call
- * only. n = 0 is skipped. Pointers need their element type's alignment;
+ *   A moment that is not finite has the NaN code. Zero bytes are a valid start
+ *   (all moments 0).
+ * Pointers are of the current device. The table is read during the call only;
+ * tensors of n = 0 are skipped. Pointers need their element type's alignment;
  * tensors whose pointers are all aligned to 8 elements (32 bytes for float32,
  * 16 for bf16, 8 for codes) are read in wide accesses. Memory that is written may not overlap any other range of
  * the call (SVLA_ERR_ARG), so no tensor may be listed twice; gradients may be
  * shared.
  *   step_device, lr_device: NULL, or a device int64 / double read when the step
- *     runs instead of `step` / `lr`: a captured and replayed call then takes
- *     each replay's values (the host's are fixed at capture).
+ *     runs instead of `step` / `lr` (the step number counts from 1): a captured
+ *     and replayed call then takes each replay's values (the host's are fixed
+ *     at capture).
  *   workspace: device, 8-byte aligned, svla_op_adamw_workspace_bytes(n_tensors)
  *     bytes, with a clip only (else NULL); nothing is kept in it between calls.
  *     Calls that may overlap on the GPU, replayed graphs among them, need

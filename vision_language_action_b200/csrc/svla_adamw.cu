@@ -319,7 +319,7 @@ SVLA_DEV uint32_t v_field(uint32_t vx) { return (uint32_t)max((int)(vx >> 23) - 
 
 // The 8-bit step of a warp's block whatever its values: a zero v, moments near
 // the ends of fp32's range, or ones that are not finite (they take the NaN
-// code; the scales are those of the finite ones).
+// code, and so would a negative v; the scales are those of the others).
 template <typename TP, typename TG>
 SVLA_DEV void general8(const AdamwCoefs& c, const Place<TP, TG, uint8_t>& a, const uint32_t (&r)[4]) {
   Loaded<TP, TG, uint8_t> in;
@@ -339,7 +339,7 @@ SVLA_DEV void general8(const AdamwCoefs& c, const Place<TP, TG, uint8_t>& a, con
     p[j] = value(in.p, j);
     update1(c, a.keep, a.isb2, a.step_size, __fmul_rn(value(in.g, j), a.clip), p[j], m[j], v[j]);
     if (magnitude(m[j]) < INF_MAG) mx = max(mx, magnitude(m[j]));
-    if (magnitude(v[j]) < INF_MAG) vx = max(vx, magnitude(v[j]));
+    if (v[j] >= 0.f && magnitude(v[j]) < INF_MAG) vx = max(vx, magnitude(v[j]));
   }
   mx = __reduce_max_sync(0xffffffffu, mx);
   vx = __reduce_max_sync(0xffffffffu, vx);
@@ -349,7 +349,7 @@ SVLA_DEV void general8(const AdamwCoefs& c, const Place<TP, TG, uint8_t>& a, con
   for (int j = 0; j < 8; ++j) {
     const uint32_t u20 = (j & 1) ? (r[j >> 1] >> 12) & 0xffff0u : (r[j >> 1] & 0xffffu) << 4;
     mc[j] = magnitude(m[j]) >= INF_MAG ? 0x7fu : encode_m(m[j], u20, em << 3);
-    vc[j] = magnitude(v[j]) >= INF_MAG ? 0x7fu : encode_v(v[j], u20, ev << 2);
+    vc[j] = v[j] >= 0.f && magnitude(v[j]) < INF_MAG ? encode_v(v[j], u20, ev << 2) : 0x7fu;
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {

@@ -447,7 +447,8 @@ class AdamW:
     parameter whether ``weight_decay`` applies (default: to all). ``state`` = (m, v, m_scale, v_scale), lists of
     tensors (the scales None with 32 bits), resumes with those moments and ``step`` with that many steps taken.
     ``capturable`` counts the steps on the device, so that a captured ``step`` counts on at every replay; ``lr``
-    may then be a float64 CUDA tensor of one element, read at every step.
+    may then be a float64 CUDA tensor of one element, read at every step. A step without it that is captured repeats
+    its own step number at every replay.
     """
 
     def __init__(self, params: Sequence[torch.Tensor], lr=1e-3, betas: Tuple[float, float] = (0.9, 0.999),
@@ -468,6 +469,7 @@ class AdamW:
         self._check(self.params, size, self.params[0].dtype, self.params[0].get_device(), "parameters")
         self.device, self.state_bits, self.lr, self.steps = dev, state_bits, lr, int(step)
         self._dev = self.params[0].get_device()
+        own: List[Optional[torch.Tensor]] = []
         per = [(k + 255) // 256 for k in size]
         kinds = (torch.float32, torch.float32) if state_bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
         if state is None:
@@ -476,8 +478,13 @@ class AdamW:
             for k in size:
                 at.append(at[-1] + (k + 7) // 8 * 8)
             flat = [torch.zeros(at[-1] * (state_bits // 8), dtype=torch.uint8, device=dev).view(k) for k in kinds]
+            own += flat
             state = [[f[a:a + k] for a, k in zip(at, size)] for f in flat]
-            state += [None, None] if state_bits == 32 else [torch.zeros(sum(per), device=dev).split(per) for _ in "mv"]
+            if state_bits == 32:
+                state += [None, None]
+            else:
+                own += [torch.zeros(sum(per), device=dev) for _ in "mv"]
+                state += [f.split(per) for f in own[2:]]
         self.m, self.v, self.m_scale, self.v_scale = (None if x is None else list(x) for x in state)
         self.copies = [None] * n if copies is None else list(copies)
         flags = [True] * n if decay is None else [bool(d) for d in decay]
@@ -506,6 +513,8 @@ class AdamW:
         a.param_type, a.state_bits = _type(self.params[0], "parameters"), state_bits
         (a.beta1, a.beta2), a.eps, a.weight_decay, a.max_norm, a.seed = betas, eps, weight_decay, max_norm, seed
         a.step_device = self.step_tensor.data_ptr() if capturable else None
+        # what this object allocated: told to the allocator where a step runs on a stream given
+        self._own = [t for t in own + [self._ws, self.grad_norm, self.step_tensor] if t is not None]
         self._args_ref, self._ws_bytes = ctypes.byref(a), ws
         self._ws_ptr = self._ws.data_ptr() if ws else None
         self._norm_ptr = self.grad_norm.data_ptr() if max_norm else None
@@ -545,6 +554,9 @@ class AdamW:
             on = stream if stream is not None else torch.cuda.current_stream(self.device)
             with torch.cuda.stream(on):
                 self.step_tensor.add_(1)
+        if stream is not None:
+            for t in self._own:
+                t.record_stream(stream)
         st = _launch(self._dev, stream, self.lib.svla_op_adamw, self._table_ptr, len(self._size), self._args_ref, self._ws_ptr,
                      self._ws_bytes, self._norm_ptr)
         if st:
