@@ -245,6 +245,9 @@ __global__ void __launch_bounds__(NU <= 2 ? 1024 : 512) layernorm_kernel(const L
   griddep_wait();  // nothing is read before: the weights may come from an optimiser step
   const int T = a.T, tid = threadIdx.x % T, D = a.D;
   const long long row = (long long)blockIdx.x * (blockDim.x / T) + threadIdx.x / T;
+  const bool active = row < a.M;
+  RowRegs<TX, NU, STEP> x;
+  x.load(reinterpret_cast<const TX*>(a.x) + (active ? row : 0) * a.ldx, D, T, tid);
   // columns of this thread's warp (or part of one): whole units of 256, the last one cut
   const int width = min(T, 32);
   float cnt = (float)D, inv_cnt = a.inv_d;
@@ -255,9 +258,6 @@ __global__ void __launch_bounds__(NU <= 2 ? 1024 : 512) layernorm_kernel(const L
     cnt = (float)mine;
     inv_cnt = mine ? 1.f / cnt : 0.f;
   }
-  const bool active = row < a.M;
-  RowRegs<TX, NU, STEP> x;
-  x.load(reinterpret_cast<const TX*>(a.x) + (active ? row : 0) * a.ldx, D, T, tid);
   f32x2 s2 = both(0.f);
 #pragma unroll
   for (int u = 0; u < NU; ++u)
