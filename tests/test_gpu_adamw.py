@@ -510,3 +510,26 @@ def test_a_negative_second_moment_stays_in_its_element():
     assert torch.equal(a["m"][0].view(torch.uint8), b["m"][0].view(torch.uint8))
     assert torch.equal(a["v"][0].view(torch.uint8)[keep][256:], b["v"][0].view(torch.uint8)[keep][256:])
     assert torch.allclose(a["p"][0][keep], b["p"][0][keep], rtol=1e-6)
+
+
+@pytest.mark.parametrize("N", [16, 64, 4096])
+@pytest.mark.parametrize("max_norm", [0.0, 1.0])
+def test_copies_as_the_weights_of_the_next_product(N, max_norm):
+    """The bf16 copy taken as the W of svla_op_gemm right behind the step, which fetches it as early as it may. As a
+    graph, without the host's time between."""
+    from vision_language_action_b200.runtime import op_gemm
+    K = 1024
+    gen = torch.Generator().manual_seed(2)
+    start, g = torch.randn(N, K, generator=gen).to(DEV), torch.randn(N, K, generator=gen).to(DEV)
+    lhs = torch.randn(64, K, generator=gen).to(torch.bfloat16).to(DEV)
+    p, copy, out = start.clone(), torch.zeros(N, K, dtype=torch.bfloat16, device=DEV), torch.empty(64, N, device=DEV)
+    opt = AdamW([p], lr=0.5, max_norm=max_norm, copies=[copy], capturable=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step([g])
+        op_gemm("f32", lhs, copy, out, splits=1)
+    for _ in range(5):
+        graph.replay()
+        torch.cuda.synchronize()
+        early = out.clone()
+        assert torch.equal(early, op_gemm("f32", lhs, copy, out, splits=1))

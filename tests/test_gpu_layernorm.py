@@ -18,7 +18,7 @@ torch = pytest.importorskip("torch")
 
 from oracle import optim as oo  # noqa: E402
 from vision_language_action_b200 import _abi  # noqa: E402
-from vision_language_action_b200.runtime import AdamW, op_layernorm, op_layernorm_backward  # noqa: E402
+from vision_language_action_b200.runtime import AdamW, op_gemm, op_layernorm, op_layernorm_backward  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -256,3 +256,31 @@ def test_norm_backward_and_optimiser_together():
         # m / sqrt(v) keeps the gradients' relative error (1e-6 of sum|terms|, up to 1e-3 of a sum that cancels)
         assert np.abs(np64(gain) - p[0]).max() <= 1e-2 * step * 2e-3 and np.abs(np64(bias) - p[1]).max() <= 1e-2 * step * 2e-3
         assert torch.equal(a["gamma"], gain.to(torch.bfloat16)) and torch.equal(a["beta"], bias.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("M", [16, 64, 4096])
+def test_outputs_as_the_weights_of_the_next_product(M):
+    """svla_op_gemm fetches W before the kernel ahead of it has ended, where that one lets it start early: y and dx
+    taken as W right behind the call give what they give after a wait. As graphs, without the host's time between."""
+    D = 1024
+    a = make(M, D, x="bf16", y="bf16", seed=4)
+    lhs = (torch.randn(64, D, generator=torch.Generator().manual_seed(1)) * 0.1).to(torch.bfloat16).to(DEV)
+    out = torch.empty(64, M, device=DEV)
+    calls = [lambda: op_layernorm(a["x"], a["gamma"], a["beta"], a["y"], 1e-5, a["mean"], a["rstd"]),
+             lambda: op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"], a["rstd"], a["dx"]),
+             lambda: op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"], a["rstd"], a["dx"], a["dgamma"],
+                                           a["dbeta"])]
+    for call, name in zip(calls, ("y", "dx", "dx")):
+        call()
+        torch.cuda.synchronize()
+        want = op_gemm("f32", lhs, a[name], out, splits=1).clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+            op_gemm("f32", lhs, a[name], out, splits=1)
+        for _ in range(5):
+            a[name].fill_(3.0)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)

@@ -241,7 +241,7 @@ struct Moments {
 template <typename TX, typename TY, typename TW, int NU, int STEP>
 __global__ void __launch_bounds__(NU <= 2 ? 1024 : 512) layernorm_kernel(const LnArgs a) {
   __shared__ Moments red[32];
-  griddep_launch_dependents();
+  // no early launch of dependents: y may be the W of the GEMM that follows, which fetches it before its wait
   griddep_wait();  // nothing is read before: the weights may come from an optimiser step
   const int T = a.T, tid = threadIdx.x % T, D = a.D;
   const long long row = (long long)blockIdx.x * (blockDim.x / T) + threadIdx.x / T;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(STEP == STEP_T ? 256 : 512)
   // its way to L2 (16384 x 2048 fp32: 70 us, 77 without)
   constexpr int ROW = NU * 2 * (int)(sizeof(TX) + sizeof(TY));
   constexpr bool PREFETCH = STEP == VEC8 && !SMEM_ACC && 2 * ROW + 16 * NU <= 80;
-  griddep_launch_dependents();
+  if (gridDim.x > 1 && (a.dgamma || a.dbeta)) griddep_launch_dependents();  // layernorm_cols_kernel, which waits first
   griddep_wait();
   const int T = a.T, tid = threadIdx.x % T, D = a.D, R = blockDim.x / T, group = threadIdx.x / T;
   const int W = NU * 8 * T;  // slots
@@ -467,7 +467,6 @@ template <int STEP>
 __global__ void __launch_bounds__(1024) layernorm_cols_kernel(const float* partial, int blocks, int D, int W, int T,
                                                               float* dgamma, float* dbeta) {
   __shared__ float part[32][33];
-  griddep_launch_dependents();
   griddep_wait();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
