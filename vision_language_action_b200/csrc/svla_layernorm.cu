@@ -73,7 +73,7 @@ LnPlan ln_fwd_plan(int D, bool vec, bool bf16_x) {
 LnPlan ln_bwd_plan(int D) { return D <= 768 ? ln_plan(D, 3, 32) : ln_plan(D, D <= 8192 ? 2 : 3, 512); }
 
 int ln_bwd_blocks(int M, const LnPlan& p, int per_sm) {
-  return std::min((M + p.R - 1) / p.R, LN_SMS * std::min(per_sm, LN_BWD_PER_SM));
+  return std::min((M - 1) / p.R + 1, LN_SMS * std::min(per_sm, LN_BWD_PER_SM));
 }
 size_t ln_bwd_workspace(int M, int D) {
   const LnPlan p = ln_bwd_plan(D);
@@ -597,7 +597,7 @@ svla_status run(LnArgs& a, int xt, int yt, int wt, bool bwd, bool vec, cudaStrea
   const int W = p.NU * 8 * p.T;
   const size_t full = bwd ? (size_t)(p.smem_acc ? 1 : p.R) * 2 * W * sizeof(float) : 0;
   const size_t smem = p.smem_acc || a.dgamma || a.dbeta ? full : 0;
-  int blocks = (a.M + p.R - 1) / p.R;
+  int blocks = (a.M - 1) / p.R + 1;
   cudaError_t e = cudaSuccess;
   if (full > 40 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)full);
   if (e == cudaSuccess && bwd && blocks > 1) {
