@@ -284,3 +284,18 @@ def test_outputs_as_the_weights_of_the_next_product(M):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("D", [8, 100, 768, 1100, 1283, 5000, 8200, 12288])
+@pytest.mark.parametrize("value", [1e-30, 1.0, 2e19, 1e30])
+def test_constant_rows_of_any_size(D, value):
+    """The mean of a constant row is the value within the sum's rounding, 64 2^-24 of it, and its differences from that
+    mean are no larger; where their squares are within float32, so is all that follows."""
+    x = torch.full((3, D), value, device=DEV)
+    y, mean, rstd = torch.empty_like(x), torch.empty(3, device=DEV), torch.empty(3, device=DEV)
+    op_layernorm(x, torch.ones(D, device=DEV), None, y, 1e-5, mean, rstd)
+    assert (mean.double() / value - 1).abs().max() <= 64 * 2.0 ** -24
+    off = 64 * 2.0 ** -24 * value
+    if off < 1e18:
+        assert torch.isfinite(y).all() and torch.isfinite(rstd).all()
+        assert (rstd.double() * (1e-5 ** 0.5)).max() <= 1 + 1e-5 and rstd.double().min() >= (off ** 2 + 1e-5) ** -0.5 * (1 - 1e-5)

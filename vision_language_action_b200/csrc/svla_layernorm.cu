@@ -216,7 +216,7 @@ struct Moments {
   SVLA_DEV void merge(const Moments& o) {
     const float all = n + o.n, part = all > 0.f ? __fdividef(o.n, all) : 0.f, d = o.mean - mean;
     mean = fmaf(d, part, mean);
-    m2 = m2 + o.m2 + d * d * n * part;
+    m2 = m2 + o.m2 + d * (d * (n * part));  // n part first: 0 with an empty set, however large the other's mean
     n = all;
   }
   SVLA_DEV void merge_lanes(int from, int below) {  // butterfly over distances from .. 1 that are below `below`
