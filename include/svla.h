@@ -450,7 +450,8 @@ SVLA_API svla_status svla_op_rmsnorm(const float* x, const void* g, int M, int D
  *     alignment fix: results are bitwise reproducible.
  *   y may be x itself and dx may be x or dy itself (same pointer, type and
  *     stride); any other overlap of an output with another argument is
- *     SVLA_ERR_ARG.
+ *     SVLA_ERR_ARG. Matrices of one row pitch whose rows lie between each
+ *     other's (the halves of a wider matrix) do not overlap.
  *   M >= 0 (M = 0 writes no rows and zero gradients), 1 <= D <= 16384, eps > 0.
  *   workspace: device, 4-byte aligned, at least
  *     svla_op_layernorm_backward_workspace_bytes(M, D) bytes (0 for few rows,

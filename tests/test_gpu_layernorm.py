@@ -299,3 +299,26 @@ def test_constant_rows_of_any_size(D, value):
     if off < 1e18:
         assert torch.isfinite(y).all() and torch.isfinite(rstd).all()
         assert (rstd.double() * (1e-5 ** 0.5)).max() <= 1 + 1e-5 and rstd.double().min() >= (off ** 2 + 1e-5) ** -0.5 * (1 - 1e-5)
+
+
+@pytest.mark.parametrize("D", [64, 771, 2048])
+@pytest.mark.parametrize("order", [(0, 1, 2), (2, 0, 1), (1, 2, 0)])
+def test_parts_of_one_wider_matrix(D, order):
+    """x, dy and the output as the column blocks of one buffer, in any order: their rows lie between each other's."""
+    M = 33
+    a = make(M, D, seed=6)
+    wide = torch.full((M, 3 * D), 5.0, device=DEV)
+    x, dy, out = (wide[:, k * D:(k + 1) * D] for k in order)
+    x.copy_(a["x"])
+    dy.copy_(a["dy"])
+    op_layernorm(a["x"], a["gamma"], a["beta"], a["y"], 1e-5, a["mean"], a["rstd"])
+    op_layernorm(x, a["gamma"], a["beta"], out, 1e-5)
+    tol = dict(rtol=0, atol=2e-5 * float(a["y"].abs().max()))  # odd widths: other threads hold the elements
+    assert torch.allclose(out, a["y"], **tol)
+    op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"], a["rstd"], a["dx"])
+    op_layernorm_backward(dy, x, a["gamma"], a["mean"], a["rstd"], out)
+    assert torch.allclose(out, a["dx"], rtol=0, atol=2e-5 * float(a["dx"].abs().max()))
+    assert torch.equal(x, a["x"]) and torch.equal(dy, a["dy"])
+    with pytest.raises(_abi.SvlaError):
+        op_layernorm(x, a["gamma"], a["beta"], wide[:, 1 + order[0] * D:1 + order[0] * D + D] if order[0] < 2 else
+                     wide[:, D + D // 2:2 * D + D // 2], 1e-5)

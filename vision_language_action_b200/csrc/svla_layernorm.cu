@@ -569,9 +569,16 @@ struct Mat {
   bool same(const Mat& o) const { return p == o.p && ld == o.ld && type == o.type; }
 };
 bool overlap(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) { return a0 < b1 && b0 < a1; }
+// rows of one pitch that lie between each other's rows, as the halves of a wider matrix do
+bool between(const Mat& a, const Mat& b, int D) {
+  const size_t pitch = a.ld * bytes_of(a.type);
+  if (pitch != b.ld * bytes_of(b.type)) return false;
+  const size_t from = a.begin() <= b.begin() ? (b.begin() - a.begin()) % pitch : (pitch - (a.begin() - b.begin()) % pitch) % pitch;
+  return from >= D * bytes_of(a.type) && from + D * bytes_of(b.type) <= pitch;
+}
 // an output may be an input matrix itself (each row is read before it is written), not a part of it
 bool clash(const Mat& out, const Mat& in, int M, int D) {
-  return !out.same(in) && overlap(out.begin(), out.end(M, D), in.begin(), in.end(M, D));
+  return !out.same(in) && overlap(out.begin(), out.end(M, D), in.begin(), in.end(M, D)) && !between(out, in, D);
 }
 bool clash(const Mat& out, const void* v, size_t bytes, int M, int D) {
   return v && overlap(out.begin(), out.end(M, D), (uintptr_t)v, (uintptr_t)v + bytes);
