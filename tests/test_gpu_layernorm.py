@@ -322,3 +322,24 @@ def test_parts_of_one_wider_matrix(D, order):
     with pytest.raises(_abi.SvlaError):
         op_layernorm(x, a["gamma"], a["beta"], wide[:, 1 + order[0] * D:1 + order[0] * D + D] if order[0] < 2 else
                      wide[:, D + D // 2:2 * D + D // 2], 1e-5)
+
+
+def test_row_counts_and_strides_at_the_end_of_32_bits():
+    buf = torch.zeros(2 ** 31 + 64, dtype=torch.bfloat16, device=DEV)
+    one, beta = torch.ones(1, device=DEV), torch.full((1,), 0.5, device=DEV)
+    x = buf[:2 ** 31 - 100].view(-1, 1)
+    op_layernorm(x, one, beta, x, 1e-5)  # a row of one element has no variance: y = beta
+    assert (x[:1000] == 0.5).all() and (x[-1000:] == 0.5).all() and (x[2 ** 30:2 ** 30 + 1000] == 0.5).all()
+    assert not buf[2 ** 31 - 100:].any()
+    g8 = torch.ones(8, device=DEV)
+    for bad, g in ((buf.view(-1, 1), one), (buf.as_strided((2, 8), (2 ** 31 + 8, 1)), g8)):
+        with pytest.raises(ValueError):
+            op_layernorm(bad, g, None, bad)
+    # rows that lie further than 2^32 bytes apart
+    far = buf.as_strided((2, 8), (2 ** 31 - 8, 1))
+    v = torch.randn(2, 8, device=DEV).to(torch.bfloat16)
+    far.copy_(v)
+    y = torch.empty_like(v)
+    op_layernorm(v, g8, None, y)
+    op_layernorm(far, g8, None, far)
+    assert torch.equal(far, y)

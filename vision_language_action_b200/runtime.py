@@ -360,6 +360,8 @@ def _rows(t: torch.Tensor, M: int, D: int, dev: int, what: str):
         ld = D
     if (D > 1 and one != 1) or ld < D:
         raise ValueError(f"{what}: rows must be contiguous and apart")
+    if max(M, D, ld) > 0x7fffffff:  # the C arguments are ints
+        raise ValueError(f"{what}: fewer than 2^31 rows, columns and elements between rows expected")
     return t.data_ptr(), _type(t, what), ld
 
 
