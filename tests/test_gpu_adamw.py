@@ -533,3 +533,17 @@ def test_copies_as_the_weights_of_the_next_product(N, max_norm):
         torch.cuda.synchronize()
         early = out.clone()
         assert torch.equal(early, op_gemm("f32", lhs, copy, out, splits=1))
+
+
+def test_train_weights_into_a_given_tensor():
+    s, wb, _ = tiny_case()
+    m = SmolVLA(s, synth.pack_blob(s, wb), max_batch=2, max_prefix=24, max_chunk=8, train=True)
+    try:
+        want = m.train_weights()
+        out = torch.zeros_like(want)
+        assert m.train_weights(out) is out and torch.equal(out, want)
+        for bad in (torch.zeros(2 * want.numel(), dtype=torch.bfloat16, device=DEV)[::2], out.cpu(), out[:-1], out.float()):
+            with pytest.raises(ValueError):
+                m.train_weights(bad)
+    finally:
+        m.close()

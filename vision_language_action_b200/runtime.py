@@ -207,9 +207,8 @@ class SmolVLA:
             out = torch.empty(n, dtype=torch.bfloat16, device=f"cuda:{self.device}")
             if stream is not None:
                 out.record_stream(stream)
-        elif out.dtype != torch.bfloat16 or out.numel() != n:
-            raise ValueError(f"out: {n} bfloat16 elements expected")
-        _abi.check(self.lib.svla_train_weights(self.h, _ptr(out), _stream(stream)), self.h)
+        _abi.check(self.lib.svla_train_weights(self.h, _vec(out, n, "out", torch.bfloat16, self.device),
+                                               _stream(stream)), self.h)
         return out
 
     def new_moments(self, state_bits: int = 32):
