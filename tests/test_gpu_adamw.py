@@ -547,3 +547,25 @@ def test_train_weights_into_a_given_tensor():
                 m.train_weights(bad)
     finally:
         m.close()
+
+
+def test_parameters_whose_storage_was_replaced():
+    """`.data = ..` between steps, as moving or reloading a module does: the step goes to the storage of the moment,
+    never to the old one, and refuses one of another type or size."""
+    p, q, g = torch.ones(100, device=DEV), torch.ones(100, device=DEV), torch.full((100,), 0.1, device=DEV)
+    copy = torch.zeros(100, dtype=torch.bfloat16, device=DEV)
+    opt, ref = AdamW([p], lr=1e-2, copies=[copy]), AdamW([q], lr=1e-2)
+    opt.step([g]), ref.step([g])
+    old, old_copy = p.data, copy.data
+    keep, keep_copy = old.clone(), old_copy.clone()
+    p.data, copy.data = old.clone(), torch.zeros_like(copy)
+    opt.step([g]), ref.step([g])
+    assert torch.equal(old, keep) and torch.equal(old_copy, keep_copy)
+    assert torch.equal(p, q) and torch.equal(copy, q.to(torch.bfloat16))
+    for bad in (torch.ones(100, dtype=torch.bfloat16, device=DEV), torch.ones(99, device=DEV),
+                torch.ones(200, device=DEV)[::2], torch.ones(100)):
+        other = torch.ones(100, device=DEV)
+        opt = AdamW([other])
+        other.data = bad
+        with pytest.raises(ValueError):
+            opt.step([g])

@@ -444,12 +444,13 @@ class AdamW:
     ``state_bits`` 32 keeps the moments in float32, 8 in float8_e4m3fn (m) and float8_e5m2 (v) with one float32
     scale for 256 elements, stochastically rounded from ``seed``. ``max_norm`` > 0 clips by the norm over all
     gradients (left in ``grad_norm``, float32 [1], by every step; a step whose norm is not finite changes nothing
-    else). ``copies`` (bfloat16, one a parameter) receive the updated parameters rounded. ``decay`` says for each
+    else, but counts). ``copies`` (bfloat16, one a parameter) receive the updated parameters rounded. ``decay`` says for each
     parameter whether ``weight_decay`` applies (default: to all). ``state`` = (m, v, m_scale, v_scale), lists of
     tensors (the scales None with 32 bits), resumes with those moments and ``step`` with that many steps taken.
     ``capturable`` counts the steps on the device, so that a captured ``step`` counts on at every replay; ``lr``
     may then be a float64 CUDA tensor of one element, read at every step. A step without it that is captured repeats
-    its own step number at every replay.
+    its own step number at every replay. Autograd does not see the parameters change: step between a backward pass and
+    the next forward, not between a forward and its backward pass.
     """
 
     def __init__(self, params: Sequence[torch.Tensor], lr=1e-3, betas: Tuple[float, float] = (0.9, 0.999),
@@ -494,14 +495,15 @@ class AdamW:
         # the C table, as an array whose columns are filled at once
         self._size, self._table = size, np.zeros(n, dtype=np.dtype(_abi.SvlaAdamwTensor))
         self._table_ptr = ctypes.cast(self._table.ctypes.data, ctypes.POINTER(_abi.SvlaAdamwTensor))
-        columns = [("param", self.params, size, self.params[0].dtype), ("m", self.m, size, kinds[0]),
-                   ("v", self.v, size, kinds[1]), ("copy", self.copies, size, torch.bfloat16)]
+        columns = [("m", self.m, size, kinds[0]), ("v", self.v, size, kinds[1])]
         if state_bits == 8:
             columns += [("m_scale", self.m_scale, per, torch.float32), ("v_scale", self.v_scale, per, torch.float32)]
         for column, ts, sizes, kind in columns:
-            if column != "param":
-                self._check(ts, sizes, kind, self._dev, column, column == "copy")
-            self._table[column] = [0 if t is None else t.data_ptr() for t in ts]
+            self._check(ts, sizes, kind, self._dev, column)
+            self._table[column] = [t.data_ptr() for t in ts]
+        self._dtype = self.params[0].dtype
+        self._watched = self.params + [t for t in self.copies if t is not None]
+        self._bind()
         self._table["n"], self._table["decay"] = size, flags
         self.capturable = capturable
         self.step_tensor = torch.full((1,), self.steps, dtype=torch.int64, device=dev) if capturable else None
@@ -532,6 +534,14 @@ class AdamW:
                 raise ValueError(f"{what} of parameter {i}: a contiguous tensor of {k} {dtype} elements on "
                                  f"cuda:{dev} expected")
 
+    def _bind(self) -> None:
+        """Addresses of the parameters and copies into the table."""
+        self._check(self.params, self._size, self._dtype, self._dev, "parameters")
+        self._check(self.copies, self._size, torch.bfloat16, self._dev, "copy", True)
+        self._table["param"] = [t.data_ptr() for t in self.params]
+        self._table["copy"] = [0 if t is None else t.data_ptr() for t in self.copies]
+        self._at = [t.data_ptr() for t in self._watched]
+
     def _check_lr(self, lr: torch.Tensor) -> None:
         if not self.capturable or lr.dtype != torch.float64 or lr.device != self.device or lr.numel() != 1:
             raise ValueError("a tensor lr: one float64 on the parameters' device, with capturable")
@@ -541,6 +551,8 @@ class AdamW:
         if len(grads) == 0:
             raise ValueError("no gradients")
         self._check(grads, self._size, grads[0].dtype, self._dev, "gradients")
+        if [t.data_ptr() for t in self._watched] != self._at:  # a parameter was given other storage (`.data = ..`)
+            self._bind()
         self._table["grad"] = [g.data_ptr() for g in grads]
         a = self._args
         a.grad_type = _type(grads[0], "gradients")
