@@ -569,3 +569,11 @@ def test_parameters_whose_storage_was_replaced():
         other.data = bad
         with pytest.raises(ValueError):
             opt.step([g])
+
+
+def test_a_missing_gradient_is_refused():
+    p = [torch.zeros(10, device=DEV), torch.zeros(6, device=DEV)]
+    opt = AdamW(p)
+    with pytest.raises(ValueError):
+        opt.step([torch.zeros(10, device=DEV), None])
+    assert opt.steps == 0 and not p[0].any()

@@ -6,6 +6,8 @@ to own device memory and to name the current CUDA stream.
 from __future__ import annotations
 
 import ctypes
+import functools
+import operator
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -350,16 +352,17 @@ def _type(t: torch.Tensor, what: str) -> int:
     return kind
 
 
-def _rows(t: torch.Tensor, M: int, D: int, dev: int, what: str):
-    """(address, type, row stride) of a [M, D] matrix on device `dev` whose rows are contiguous."""
-    if t.get_device() != dev or dev < 0 or t.dim() != 2 or t.shape[0] != M or t.shape[1] != D:
-        raise ValueError(f"{what}: a CUDA matrix of shape {(M, D)} on x's device expected")
+def _rows(t: torch.Tensor, shape: torch.Size, dev: int, what: str):
+    """(address, type, row stride) of a matrix of that shape on device `dev` whose rows are contiguous."""
+    if t.get_device() != dev or dev < 0 or t.shape != shape:
+        raise ValueError(f"{what}: a CUDA matrix of shape {tuple(shape)} on x's device expected")
+    M, D = shape
     ld, one = t.stride()
     if M <= 1:
         ld = D
-    if (D > 1 and one != 1) or ld < D:
+    if (one != 1 and D > 1) or ld < D:
         raise ValueError(f"{what}: rows must be contiguous and apart")
-    if max(M, D, ld) > 0x7fffffff:  # the C arguments are ints
+    if M > 0x7fffffff or ld > 0x7fffffff:  # the C arguments are ints
         raise ValueError(f"{what}: fewer than 2^31 rows, columns and elements between rows expected")
     return t.data_ptr(), _type(t, what), ld
 
@@ -401,15 +404,21 @@ def op_layernorm(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tens
     lib = _abi.load()
     if x.dim() != 2:
         raise ValueError("x: a [M, D] matrix expected")
-    (M, D), dev, f32 = x.shape, x.get_device(), torch.float32
-    px, tx, ldx = _rows(x, M, D, dev, "x")
-    py, ty, ldy = _rows(y, M, D, dev, "y")
+    shape, dev, f32 = x.shape, x.get_device(), torch.float32
+    M, D = shape
+    px, tx, ldx = _rows(x, shape, dev, "x")
+    py, ty, ldy = _rows(y, shape, dev, "y")
     st = _launch(dev, stream, lib.svla_op_layernorm, px, tx, ldx, _vec(gamma, D, "gamma", None, dev),
                  _vec(beta, D, "beta", gamma.dtype, dev), _type(gamma, "gamma"), M, D, eps, py, ty, ldy,
                  _vec(mean, M, "mean", f32, dev), _vec(rstd, M, "rstd", f32, dev))
     if st:
         _abi.check(st)
     return y
+
+
+@functools.lru_cache(maxsize=256)
+def _layernorm_workspace(M: int, D: int) -> int:
+    return int(_abi.load().svla_op_layernorm_backward_workspace_bytes(M, D))
 
 
 def op_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, mean: torch.Tensor,
@@ -419,15 +428,16 @@ def op_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor
     lib = _abi.load()
     if x.dim() != 2:
         raise ValueError("x: a [M, D] matrix expected")
-    (M, D), dev, f32 = x.shape, x.get_device(), torch.float32
-    px, tx, ldx = _rows(x, M, D, dev, "x")
-    pdy, ty, lddy = _rows(dy, M, D, dev, "dy")
-    pdx, tdx, lddx = _rows(dx, M, D, dev, "dx")
+    shape, dev, f32 = x.shape, x.get_device(), torch.float32
+    M, D = shape
+    px, tx, ldx = _rows(x, shape, dev, "x")
+    pdy, ty, lddy = _rows(dy, shape, dev, "dy")
+    pdx, tdx, lddx = _rows(dx, shape, dev, "dx")
     if tdx != tx:
         raise ValueError("dx must have x's type")
     n = 0
     if dgamma is not None or dbeta is not None:
-        n = lib.svla_op_layernorm_backward_workspace_bytes(M, D)
+        n = _layernorm_workspace(M, D)
     ws = _scratch(n, x.device, stream)
     st = _launch(dev, stream, lib.svla_op_layernorm_backward, pdy, ty, lddy, px, tx, ldx,
                  _vec(gamma, D, "gamma", None, dev), _type(gamma, "gamma"), _vec(mean, M, "mean", f32, dev),
@@ -526,6 +536,14 @@ class AdamW:
     def _check(ts, sizes, dtype, dev: int, what: str, none_too: bool = False) -> None:
         if ts is None or len(ts) != len(sizes):
             raise ValueError(f"{what}: one tensor a parameter expected")
+        T = torch.Tensor
+        try:  # a step's usual way: no statement a tensor
+            if not none_too and dev >= 0 and list(map(T.numel, ts)) == sizes and \
+                    list(map(T.get_device, ts)).count(dev) == len(sizes) and all(map(T.is_contiguous, ts)) and \
+                    list(map(operator.attrgetter("dtype"), ts)).count(dtype) == len(sizes):
+                return
+        except TypeError:  # not a tensor: named below
+            pass
         for i, (t, k) in enumerate(zip(ts, sizes)):
             if t is None and none_too:
                 continue
@@ -551,9 +569,9 @@ class AdamW:
         if len(grads) == 0:
             raise ValueError("no gradients")
         self._check(grads, self._size, grads[0].dtype, self._dev, "gradients")
-        if [t.data_ptr() for t in self._watched] != self._at:  # a parameter was given other storage (`.data = ..`)
+        if list(map(torch.Tensor.data_ptr, self._watched)) != self._at:  # a parameter was given other storage (`.data = ..`)
             self._bind()
-        self._table["grad"] = [g.data_ptr() for g in grads]
+        self._table["grad"] = list(map(torch.Tensor.data_ptr, grads))
         a = self._args
         a.grad_type = _type(grads[0], "gradients")
         a.step = self.steps + 1
