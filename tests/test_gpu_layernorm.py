@@ -343,3 +343,13 @@ def test_row_counts_and_strides_at_the_end_of_32_bits():
     op_layernorm(v, g8, None, y)
     op_layernorm(far, g8, None, far)
     assert torch.equal(far, y)
+
+
+@pytest.mark.parametrize("D", [16, 51, 100, 720, 771, 1024, 2048, 12296, 16384])
+def test_few_rows_in_the_backward(D):
+    """One block, one cluster of 2 to 8 blocks, and the first count past it, for every number of rows a block takes."""
+    units = (D + 7) // 8
+    T = 1 << (units - 1).bit_length() if units <= 16 else 32
+    R = 256 // T if D <= 768 else 1
+    for M in sorted({1, 2, 3, R, R + 1, 2 * R, 5 * R - 1, 8 * R, 8 * R + 1}):
+        check(M, D, y="bf16", seed=M)
