@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(ADAMW_THREADS, BITS == 8 && sizeof(TP) == 2 ? 
                                                               float* __restrict__ grad_norm) {
   typedef typename std::conditional<BITS == 32, float, uint8_t>::type TS;
   // the next turn's data on its way to L2: what it saves of the loads' latency is more than its instructions cost
-  // where the parameters are fp32 (99.8 M values: 379 us, 400 without), not in bf16 (157 M: 408 us, 388 without)
+  // where the parameters are fp32 (99.8 M values: 379 us, 413 without), not in bf16 (157 M: 413 us, 381 without)
   constexpr bool PREFETCH = BITS == 8 && sizeof(TP) == 4;
   __shared__ double part[ADAMW_WARPS];
   __shared__ float s_clip;
@@ -680,7 +680,7 @@ cudaError_t resident_blocks(Fn fn, int slot, unsigned* blocks) {
 // in order keep their accesses close together in memory, where ones that stay
 // drift apart (99.8 M values: 463 us in 13 waves, 509 in one). One wave with
 // 8-bit moments: the arithmetic bounds that step, and a block's start costs it
-// about 2 us (157 M bf16 values: 368 us in one wave, 395 in 4).
+// about 2 us (157 M bf16 values: 381 us in one wave, 409 in 4).
 unsigned step_blocks(unsigned chunks, unsigned resident, int bits) {
   const unsigned waves = bits == 32 ? std::min(chunks / (8 * resident), 16u) : 1;
   return std::min(chunks, resident * std::max(waves, 1u));

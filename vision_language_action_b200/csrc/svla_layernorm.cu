@@ -251,7 +251,10 @@ __global__ void __launch_bounds__(NU <= 2 ? 1024 : 512) layernorm_kernel(const L
   const long long row = (long long)blockIdx.x * (blockDim.x / T) + threadIdx.x / T;
   const bool active = row < a.M;
   RowRegs<TX, NU, STEP> x;
-  x.load(reinterpret_cast<const TX*>(a.x) + (active ? row : 0) * a.ldx, D, T, tid);
+  // the row's loads before the count of columns where they are narrow (30000 fp32 rows of 1283: 66 us, 69 behind it),
+  // behind it where they are wide (16384 bf16 rows of 4096: 61 us, 69 before it)
+  const TX* xp = reinterpret_cast<const TX*>(a.x) + (active ? row : 0) * a.ldx;
+  if (STEP != VEC8) x.load(xp, D, T, tid);
   // columns of this thread's warp (or part of one): whole units of 256, the last one cut
   const int width = min(T, 32);
   float cnt = (float)D, inv_cnt = a.inv_d;
@@ -262,6 +265,7 @@ __global__ void __launch_bounds__(NU <= 2 ? 1024 : 512) layernorm_kernel(const L
     cnt = (float)mine;
     inv_cnt = mine ? 1.f / cnt : 0.f;
   }
+  if (STEP == VEC8) x.load(xp, D, T, tid);
   f32x2 s2 = both(0.f);
 #pragma unroll
   for (int u = 0; u < NU; ++u)
