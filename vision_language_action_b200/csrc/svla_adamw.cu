@@ -13,6 +13,14 @@
 // the device and nothing is kept between calls. A warp takes 256 consecutive
 // elements of one tensor, the block that shares a scale in the 8-bit states, 8
 // consecutive ones a lane.
+//
+// Measured (a step of 153 tensors, 99.8 M fp32 values with a bf16 copy): 32-bit
+// moments 461 us (6.5 TB/s, the rate of a copy), 540 with the clip, whose pass
+// over the gradients is 61 us of reading; 8-bit moments 300 and 378 us (6.0
+// TB/s without the clip). 144 tensors, 157 M bf16 values, 8-bit moments: 381 us,
+// 4.2 TB/s: there the instructions bound it, 55 an element where the memory's
+// time is that of about 35 (decoding, the random bits and encoding; the
+// schedulers issue in 63 % of the cycles).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -389,7 +397,8 @@ SVLA_DEV float rcp_approx(float x) {
 // ---------------------------------------------------------------------------
 // Sum of squares of the gradients: fp64 throughout, so the norm (and with it
 // the clip factor's fp32 rounding) does not depend on the order of the sum in
-// practice; fixed order all the same. partial[blockIdx.x] of this launch.
+// practice; fixed order all the same. partial[blockIdx.x] of this launch. Bound
+// by its reads (99.8 M fp32 gradients: about 70 us, 61 at the rate of a copy).
 // ---------------------------------------------------------------------------
 template <typename TG, int CAP>
 __global__ void __launch_bounds__(NORM_THREADS) grad_norm_kernel(const __grid_constant__ AdamwTable<CAP> tab,

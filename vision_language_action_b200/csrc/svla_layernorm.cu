@@ -12,6 +12,11 @@
 // 16; wider ones whole warps. With VEC a unit is 8 consecutive columns (16- and
 // 32-byte accesses); else (an odd width, stride or address) every 32nd (narrow:
 // T-th) one.
+//
+// Both are bound by memory where there are many rows, by latency where there are
+// few. Measured: forward of 65536 x 768, fp32 in and bf16 out, 51.5 us (5.9
+// TB/s); backward of 16384 rows, bf16: 768 wide 22 us (3.4 TB/s), 4096 wide 81
+// us (5.0 TB/s). One row 2.9 us, 50 rows backward 5.8 us: a launch.
 #include <algorithm>
 #include <atomic>
 #include <exception>
