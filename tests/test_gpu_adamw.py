@@ -577,3 +577,85 @@ def test_a_missing_gradient_is_refused():
     with pytest.raises(ValueError):
         opt.step([torch.zeros(10, device=DEV), None])
     assert opt.steps == 0 and not p[0].any()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_past_32_bits_of_elements(bits):
+    """2^32 + 300 elements, zero but for a stretch across 2^32 and the tensor's end, which follows the oracle with the
+    random bits of its own element numbers."""
+    from oracle.philox import philox4x32_10
+    first, n = 2 ** 32 - 512, 2 ** 32 + 300
+    k, seed, hp = n - first, 7, (1e-3, 0.9, 0.999, 1e-8, 0.1)
+    if torch.cuda.mem_get_info()[1] < 80 << 30:
+        pytest.skip("needs 60 GB")
+    part = make([k], "bf16", "bf16", bits, seed=21)
+    big = lambda dt: torch.zeros(n, dtype=torch.uint8 if dt.itemsize == 1 else dt, device=DEV).view(dt)
+    st = {key: [big(part[key][0].dtype)] for key in ("p", "g", "m", "v")}
+    per = (n + 255) // 256
+    st["ms"] = [torch.zeros(per, device=DEV)] if bits == 8 else None
+    st["vs"] = [torch.zeros(per, device=DEV)] if bits == 8 else None
+    raw = lambda t: t.view(torch.uint8)
+    for key in ("p", "g", "m", "v"):
+        raw(st[key][0])[first * st[key][0].element_size():] = raw(part[key][0])
+    if bits == 8:
+        for key in ("ms", "vs"):
+            st[key][0][first // 256:] = part[key][0]
+    M, V = start_moments(part, bits)
+    p, g = part["p"][0].float().cpu().numpy(), part["g"][0].float().cpu().numpy()
+    AdamW(st["p"], lr=hp[0], weight_decay=hp[4], state_bits=bits, seed=seed, step=4,
+          state=(st["m"], st["v"], st["ms"], st["vs"])).step(st["g"])
+    torch.cuda.synchronize()
+    for key in ("p", "m", "v"):
+        assert not raw(st[key][0])[:first * st[key][0].element_size()].any()
+    p32, m1, v1 = oo.adamw(p, g, M[0], V[0], *hp, 5, True, 1.0, dtype=np.float32)
+    tail = {key: st[key][0][first:] for key in ("p", "m", "v")}
+    if bits == 32:
+        assert np.array_equal(tail["m"].cpu().numpy(), m1) and np.array_equal(tail["v"].cpu().numpy(), v1)
+    else:
+        q = np.arange(first // 8, (n + 7) // 8, dtype=np.uint64)
+        c = (q & np.uint64(0xFFFFFFFF), q >> np.uint64(32), np.full_like(q, 5), np.zeros_like(q))
+        words = np.stack(philox4x32_10(c, (seed, 0)), axis=1)
+        u = np.stack([words & 0xFFFF, words >> 16], axis=2).reshape(-1)[:k].astype(np.int64)
+        for key, scale, x, fmt, keep in (("m", "ms", m1, oo.E4M3, False), ("v", "vs", v1, oo.E5M2, True)):
+            codes, s = oo.encode(x, u, fmt, keep)
+            assert np.array_equal(codes_of(tail[key]), codes)
+            assert np.array_equal(st[scale][0][first // 256:].cpu().numpy(), s) and not st[scale][0][:first // 256].any()
+    # bf16 parameters: half a step, beside float32's own error of the step (the docstring's bound is far below it)
+    assert (np.abs(np64(tail["p"]) - p32.astype(np.float64)) <= 2.0 ** -8 * np.abs(p32) + 1e-6).all()
+    del st, tail
+    torch.cuda.empty_cache()
+
+
+def test_two_threads_at_once():
+    """Two host threads, each with its own stream, optimiser and norm, give what each gives alone."""
+    import threading
+    from vision_language_action_b200.runtime import op_layernorm, op_layernorm_backward
+
+    def work(seed, out, stream):
+        gen = torch.Generator().manual_seed(seed)
+        p, g, xs = ([torch.randn(n, generator=gen).to(DEV) for n in ns]
+                    for ns in ((1000, 70000, 33), (1000, 70000, 33), (500 * 768, 500 * 768, 768)))
+        x, dy, gain = xs[0].view(500, 768), xs[1].view(500, 768), xs[2]
+        res = [torch.zeros_like(t) for t in (x, x, gain, gain)]
+        mean, rstd = torch.zeros(500, device=DEV), torch.zeros(500, device=DEV)
+        opt = AdamW(p, state_bits=8, max_norm=1.0, seed=seed)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            for _ in range(50):
+                opt.step(g)
+                op_layernorm(x, gain, None, res[0], 1e-5, mean, rstd)
+                op_layernorm_backward(dy, x, gain, mean, rstd, *res[1:])
+        stream.synchronize()
+        out[seed] = p + res
+
+    alone, together = {}, {}
+    for seed in (1, 2):
+        work(seed, alone, torch.cuda.Stream())
+    threads = [threading.Thread(target=work, args=(s, together, torch.cuda.Stream())) for s in (1, 2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for seed in (1, 2):
+        assert all(torch.equal(a, b) for a, b in zip(alone[seed], together[seed]))

@@ -353,3 +353,15 @@ def test_few_rows_in_the_backward(D):
     R = 256 // T if D <= 768 else 1
     for M in sorted({1, 2, 3, R, R + 1, 2 * R, 5 * R - 1, 8 * R, 8 * R + 1}):
         check(M, D, y="bf16", seed=M)
+
+
+def test_missing_arguments_are_refused():
+    a = make(4, 64)
+    with pytest.raises(ValueError):
+        op_layernorm(a["x"], None, a["beta"], a["y"])
+    with pytest.raises(ValueError):
+        op_layernorm_backward(a["dy"], a["x"], None, a["mean"], a["rstd"], a["dx"])
+    with pytest.raises(_abi.SvlaError):
+        op_layernorm_backward(a["dy"], a["x"], a["gamma"], None, a["rstd"], a["dx"])
+    with pytest.raises(ValueError):
+        op_layernorm(a["x"].reshape(2, 2, 64), a["gamma"], None, a["y"].reshape(2, 2, 64))

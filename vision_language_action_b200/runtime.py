@@ -346,6 +346,8 @@ _TYPES = {torch.float32: _abi.TYPE_F32, torch.bfloat16: _abi.TYPE_BF16}
 
 
 def _type(t: torch.Tensor, what: str) -> int:
+    if t is None:
+        raise ValueError(f"{what}: a tensor expected")
     kind = _TYPES.get(t.dtype)
     if kind is None:
         raise ValueError(f"{what}: float32 or bfloat16 expected, got {t.dtype}")
@@ -408,8 +410,9 @@ def op_layernorm(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tens
     M, D = shape
     px, tx, ldx = _rows(x, shape, dev, "x")
     py, ty, ldy = _rows(y, shape, dev, "y")
+    tw = _type(gamma, "gamma")
     st = _launch(dev, stream, lib.svla_op_layernorm, px, tx, ldx, _vec(gamma, D, "gamma", None, dev),
-                 _vec(beta, D, "beta", gamma.dtype, dev), _type(gamma, "gamma"), M, D, eps, py, ty, ldy,
+                 _vec(beta, D, "beta", gamma.dtype, dev), tw, M, D, eps, py, ty, ldy,
                  _vec(mean, M, "mean", f32, dev), _vec(rstd, M, "rstd", f32, dev))
     if st:
         _abi.check(st)
