@@ -659,3 +659,27 @@ def test_two_threads_at_once():
     torch.cuda.synchronize()
     for seed in (1, 2):
         assert all(torch.equal(a, b) for a, b in zip(alone[seed], together[seed]))
+
+
+@pytest.mark.parametrize("exponent", [90, 93, 100, 117, 118, 119])
+def test_a_first_moment_near_the_end_of_float32(exponent):
+    """m from 2^97 up to 2^127 beside an ordinary v, as no run of gradients leaves it but a given state may: the codes
+    and scales of the definition all the same. (p is beyond what m / sqrt(v) keeps in float32 and is not looked at.)"""
+    n = 700
+    gen = torch.Generator().manual_seed(exponent)
+    mc = torch.randint(0x60, 0x7F, (n,), generator=gen, dtype=torch.int64) | 0x80 * torch.randint(0, 2, (n,), generator=gen)
+    vc = torch.randint(0x20, 0x70, (n,), generator=gen, dtype=torch.int64)
+    st = dict(p=[torch.zeros(n, device=DEV)], g=[torch.randn(n, generator=gen).to(DEV)],
+              m=[mc.to(torch.uint8).to(DEV).view(torch.float8_e4m3fn)],
+              v=[vc.to(torch.uint8).to(DEV).view(torch.float8_e5m2)],
+              ms=[torch.full((3,), 2.0 ** exponent, device=DEV)], vs=[torch.full((3,), 2.0 ** -10, device=DEV)])
+    M, V = start_moments(st, 8)
+    g = st["g"][0].cpu().numpy()
+    AdamW(st["p"], state_bits=8, seed=9, step=2, state=(st["m"], st["v"], st["ms"], st["vs"])).step(st["g"])
+    _, m1, v1 = oo.adamw(np.zeros(n), g, M[0], V[0], 1e-3, 0.9, 0.999, 1e-8, 1e-2, 3, dtype=np.float32)
+    u = oo.random16(n, 0, 3, 9)
+    for got, scale, x, fmt, keep in ((st["m"][0], st["ms"][0], m1, oo.E4M3, False),
+                                     (st["v"][0], st["vs"][0], v1, oo.E5M2, True)):
+        codes, s = oo.encode(x, u, fmt, keep)
+        assert np.array_equal(scale.cpu().numpy(), s)
+        assert np.array_equal(codes_of(got), codes)

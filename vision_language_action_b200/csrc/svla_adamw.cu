@@ -381,8 +381,9 @@ SVLA_DEV void general8(const AdamwCoefs& c, const Place<TP, TG, uint8_t>& a, con
   }
 }
 
-// The usual case of the 8-bit step has v below 2^100 (its product with 2^24 is finite).
-constexpr uint32_t VX_USUAL = (127u + 100u) << 23;
+// The usual case of the 8-bit step has |m| and v below 2^100: v's product with 2^24 is finite, and the reciprocals of
+// the scales are normal numbers.
+constexpr uint32_t USUAL_MAG = (127u + 100u) << 23;
 SVLA_DEV float sqrt_approx(float x) {
   float r;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -450,7 +451,7 @@ SVLA_DEV void update32(const AdamwCoefs& c, const Place<TP, TG, float>& a) {
   store_all(a, p, in.m, in.v);
 }
 
-// The usual case in packed pairs: every v positive and below 2^100, all finite.
+// The usual case in packed pairs: every v positive, v and |m| below 2^100.
 // Else the block is done by general8.
 template <typename TP, typename TG>
 SVLA_DEV void update8(const AdamwCoefs& c, const Place<TP, TG, uint8_t>& a, uint32_t block, uint32_t step, uint32_t tensor,
@@ -488,7 +489,7 @@ SVLA_DEV void update8(const AdamwCoefs& c, const Place<TP, TG, uint8_t>& a, uint
   }
   const uint32_t mxb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
   const uint32_t vxb = __reduce_max_sync(0xffffffffu, __float_as_uint(vx));
-  if (!__all_sync(0xffffffffu, vmin > 0.f && mxb < INF_MAG && vxb < VX_USUAL)) {
+  if (!__all_sync(0xffffffffu, vmin > 0.f && mxb < USUAL_MAG && vxb < USUAL_MAG)) {
     general8(c, a, r);
     return;
   }
