@@ -365,3 +365,36 @@ def test_missing_arguments_are_refused():
         op_layernorm_backward(a["dy"], a["x"], a["gamma"], None, a["rstd"], a["dx"])
     with pytest.raises(ValueError):
         op_layernorm(a["x"].reshape(2, 2, 64), a["gamma"], None, a["y"].reshape(2, 2, 64))
+
+
+def test_workspaces_on_a_given_stream_beside_queued_work():
+    """A temporary of the workspace's size, given back while the current stream's work on it is still queued: a call on
+    another stream meanwhile takes other memory, and neither result changes. (The products' split-K scratch likewise.)"""
+    M, D = 3000, 768
+    a = make(M, D, x="bf16", y="bf16")
+    op_layernorm(a["x"], a["gamma"], a["beta"], a["y"], 1e-5, a["mean"], a["rstd"])
+    bwd = lambda s: op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"], a["rstd"], a["dx"], a["dgamma"],
+                                          a["dbeta"], stream=s)
+    gen = torch.Generator().manual_seed(3)
+    lhs, w = (torch.randn(m, 4096, generator=gen).to(torch.bfloat16).to(DEV) for m in (64, 512))
+    out = torch.empty(64, 512, device=DEV)
+    gemm = lambda s: op_gemm("f32", lhs, w, out, splits=16, stream=s)
+    lib = _abi.load()
+    sizes = [int(lib.svla_op_layernorm_backward_workspace_bytes(M, D)), int(lib.svla_op_gemm_workspace_bytes(64, 512, 4096, 16))]
+    assert min(sizes) > 0
+    bwd(None), gemm(None)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (a["dx"], a["dgamma"], a["dbeta"], out)]
+    side = torch.cuda.Stream()
+    for call, n, outs in ((bwd, sizes[0], (a["dx"], a["dgamma"], a["dbeta"])), (gemm, sizes[1], (out,))):
+        for t in outs:
+            t.fill_(7.0)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        tmp = torch.empty(n, dtype=torch.uint8, device=DEV)
+        kept = [tmp.fill_(k).sum(dtype=torch.int64) for k in range(1, 40)]
+        del tmp
+        call(side)
+        torch.cuda.synchronize()
+        assert [int(k) for k in kept] == [n * k for k in range(1, 40)]
+    assert all(torch.equal(x, y) for x, y in zip((a["dx"], a["dgamma"], a["dbeta"], out), want))

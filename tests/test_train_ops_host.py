@@ -185,3 +185,61 @@ def test_python_face_refuses_host_tensors():
         rt.AdamW([x])
     with pytest.raises(ValueError):
         rt.AdamW([])
+
+
+class FakeStream:
+    cuda_stream = 77
+
+
+@pytest.fixture
+def given_stream(monkeypatch):
+    """Streams without a GPU: yields (stream, made), the list of (bytes of a tensor made, the stream current then)."""
+    import contextlib
+    torch = pytest.importorskip("torch")
+    now, made = [None], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, now[0] = now[0], stream
+        yield
+        now[0] = before
+
+    def record(make):
+        def made_by(*size, **kw):
+            t = make(*size, **dict(kw, device="cpu"))
+            made.append((t.numel() * t.element_size(), now[0]))
+            return t
+        return made_by
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    for name in ("empty", "zeros"):
+        monkeypatch.setattr(torch, name, record(getattr(torch, name)))
+    yield FakeStream(), made
+
+
+def test_workspaces_come_from_the_pool_of_the_stream_they_are_used_on(given_stream, monkeypatch):
+    """A block that another stream's tensor gave back may still be in use there: the current stream's pool is not
+    asked for a workspace of a call on a stream given."""
+    import torch
+    from vision_language_action_b200 import runtime as rt
+    stream, made = given_stream
+    assert rt._scratch(0, "cpu", stream) is None and not made
+    rt._scratch(100, "cpu", stream), rt._scratch(50, "cpu", None)
+    assert made == [(100, stream), (50, None)]
+    # the product's split-K scratch, through a library that does nothing
+    del made[:]
+    calls = []
+
+    class Lib:
+        def svla_op_gemm_workspace_bytes(self, *a):
+            return 4096
+
+        def svla_op_gemm(self, *a):
+            calls.append(a)
+            return 0
+
+    monkeypatch.setattr(_abi, "load", Lib)
+    monkeypatch.setattr(rt, "_ptr", lambda t: None if t is None else t.data_ptr())
+    a = torch.ones(4, 64)
+    rt.op_gemm("f32", a, a, torch.ones(4, 4), splits=4, stream=stream)
+    assert made == [(4096, stream)] and calls[0][-1].value == stream.cuda_stream

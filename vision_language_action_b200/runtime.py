@@ -41,6 +41,18 @@ def _stream(stream: Optional[torch.cuda.Stream]):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _scratch(nbytes: int, device, stream, zero: bool = False) -> Optional[torch.Tensor]:
+    """A workspace of one call, from the pool of the stream that the call runs on: memory that an earlier tensor of
+    another stream gave back may still be in use by that stream's queued work."""
+    if nbytes == 0:
+        return None
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return make(nbytes, dtype=torch.uint8, device=device)
+
+
 class SmolVLA:
     """One svla_handle: weights on one GPU plus the workspace for the limits given.
 
@@ -286,7 +298,7 @@ def op_gemm(epilogue: str, A: torch.Tensor, W: torch.Tensor, C: torch.Tensor, bi
     M, K = A.shape
     N = W.shape[0]
     ws_bytes = int(lib.svla_op_gemm_workspace_bytes(M, N, K, splits))
-    ws = torch.zeros(max(ws_bytes, 16), dtype=torch.uint8, device=A.device) if ws_bytes else None
+    ws = _scratch(ws_bytes, A.device, stream, zero=True)
     st = lib.svla_op_gemm(_EPI[epilogue], _ptr(A), A.stride(0), _ptr(W), W.stride(0), M, N, K, _ptr(C), C.stride(0),
                           _ptr(bias), splits, _ptr(ws), ws_bytes, _ptr(status), _stream(stream))
     _abi.check(st)
@@ -386,16 +398,6 @@ def _launch(dev: int, stream, fn, *args) -> int:
         with torch.cuda.device(dev):
             return _launch(dev, stream, fn, *args)
     return fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
-
-
-def _scratch(nbytes: int, device, stream) -> Optional[torch.Tensor]:
-    """A workspace of one call; where the call runs on a stream other than the current one, the allocator is told."""
-    if nbytes == 0:
-        return None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
 
 
 def op_layernorm(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor], y: torch.Tensor,
