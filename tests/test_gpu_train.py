@@ -194,3 +194,31 @@ def test_train_step_needs_the_flag():
             gpu_step(m, kv_bits, valid, a, eps, t)
     finally:
         m.close()
+
+
+def test_outputs_of_calls_on_a_given_stream_beside_queued_work():
+    """What train_step and train_weights allocate for a call on a stream given is not memory that the current stream's
+    queued work still uses."""
+    s, wb, kv_bits, valid, a, eps, t = make_case("tiny", 2, 24, 8, 5)
+    m = SmolVLA(s, synth.pack_blob(s, wb), max_batch=2, max_prefix=24, max_chunk=8, train=True)
+    try:
+        kv = torch.from_numpy(kv_bits.view(np.int16)).to(DEV).view(torch.bfloat16)
+        batch = [kv] + [torch.from_numpy(x).to(DEV) for x in (valid, a, eps, t)]
+        loss, grads = m.train_step(*batch)
+        weights = m.train_weights()
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        for like, call, want in ((grads, lambda: m.train_step(*batch, stream=side), (loss, grads)),
+                                 (weights, lambda: (m.train_weights(stream=side),), (weights,))):
+            torch.cuda.synchronize()
+            torch.cuda._sleep(20_000_000)  # about 10 ms
+            tmp = torch.empty_like(like)
+            kept = [tmp.fill_(k).max() for k in range(1, 40)]
+            del tmp
+            got = call()
+            torch.cuda.synchronize()
+            assert [float(k) for k in kept] == list(range(1, 40))
+            assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert m.device_status() == _abi.SVLA_OK
+    finally:
+        m.close()

@@ -243,3 +243,55 @@ def test_workspaces_come_from_the_pool_of_the_stream_they_are_used_on(given_stre
     a = torch.ones(4, 64)
     rt.op_gemm("f32", a, a, torch.ones(4, 4), splits=4, stream=stream)
     assert made == [(4096, stream)] and calls[0][-1].value == stream.cuda_stream
+
+
+class AnyLib:
+    """A library whose every function does nothing and returns `value`."""
+
+    def __init__(self, value=0):
+        self.value, self.calls = value, []
+
+    def __getattr__(self, name):
+        def call(*a):
+            self.calls.append((name, a))
+            return 12 if name.endswith("_elems") else self.value
+        return call
+
+
+def handle_without_gpu(rt, lib):
+    import types
+    m = rt.SmolVLA.__new__(rt.SmolVLA)
+    m.lib, m.h, m.device, m.action_dim, m.asm = lib, 1, 0, 8, (4, 2)
+    m.cfg = types.SimpleNamespace(p_layers=2, p_kv_heads=1, head_dim=4, p_width=6)
+    return m
+
+
+def test_outputs_come_from_the_pool_of_the_stream_that_writes_them(given_stream, monkeypatch):
+    """Every output that a call on a stream given allocates itself, likewise; the caller's stream is told to the
+    allocator."""
+    import torch
+    from vision_language_action_b200 import runtime as rt
+    stream, made = given_stream
+    told = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: told.append(s))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
+    monkeypatch.setattr(rt, "_ptr", lambda t: None if t is None else t.data_ptr())
+    monkeypatch.setattr(rt, "_vec", lambda t, *a: t.data_ptr())
+    lib = AnyLib()
+    monkeypatch.setattr(_abi, "load", lambda: lib)
+    m = handle_without_gpu(rt, lib)
+    z = torch.ones
+    f, pad, kv = z(2, 3, 8), z(2, 5), z(4)
+    calls = [
+        (lambda: m.new_kv_cache(2, 5, stream=stream), 1), (lambda: m.prefill(f, pad, stream=stream), 1),
+        (lambda: m.denoise(kv, pad, f, 4, trace=True, stream=stream), 2),
+        (lambda: m.denoise_prefix(kv, pad, f, 4, z(2, 1, 8), trace=True, stream=stream), 2),
+        (lambda: m.sample(f, pad, 3, 3, 4, return_noise=True, stream=stream), 3),
+        (lambda: m.assemble_prefix(z(2, 1, 16, 4), z(2, 5, 6), z(2, 5), z(2, 3), stream=stream), 2),
+        (lambda: m.train_step(kv, pad, f, f, z(2), stream=stream), 2), (lambda: m.train_weights(stream=stream), 1),
+        (lambda: rt.op_quantize_affine8(z(8, 64), stream=stream), 2)]
+    for call, n in calls:
+        del made[:], told[:]
+        call()
+        assert [s for _, s in made] == [stream] * n and told == ["current"] * n
+    m.h = None

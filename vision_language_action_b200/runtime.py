@@ -53,6 +53,17 @@ def _scratch(nbytes: int, device, stream, zero: bool = False) -> Optional[torch.
         return make(nbytes, dtype=torch.uint8, device=device)
 
 
+def _new(stream, shape, dtype, device) -> torch.Tensor:
+    """An output that a call allocates itself: like its workspaces from the pool of the stream that the call runs on.
+    The allocator is told of the current stream, on which the caller will read it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 class SmolVLA:
     """One svla_handle: weights on one GPU plus the workspace for the limits given.
 
@@ -104,17 +115,17 @@ class SmolVLA:
     def kv_cache_bytes(self, B: int, L: int) -> int:
         return int(self.lib.svla_kv_cache_bytes(self.h, B, L))
 
-    def new_kv_cache(self, B: int, L: int) -> torch.Tensor:
-        """A K/V cache buffer: bf16, [2, p_layers, B, L, p_kv_heads * head_dim]."""
+    def new_kv_cache(self, B: int, L: int, stream=None) -> torch.Tensor:
+        """A K/V cache buffer: bf16, [2, p_layers, B, L, p_kv_heads * head_dim], for work on ``stream`` or on the
+        current one."""
         c = self.cfg
-        return torch.empty((2, c.p_layers, B, L, c.p_kv_heads * c.head_dim), dtype=torch.bfloat16,
-                           device=f"cuda:{self.device}")
+        return _new(stream, (2, c.p_layers, B, L, c.p_kv_heads * c.head_dim), torch.bfloat16, f"cuda:{self.device}")
 
     def prefill(self, embeds: torch.Tensor, pad_mask: torch.Tensor,
                 kv_cache: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         B, L = pad_mask.shape
         if kv_cache is None:
-            kv_cache = self.new_kv_cache(B, L)
+            kv_cache = self.new_kv_cache(B, L, stream)
         st = self.lib.svla_prefill(self.h, _ptr(embeds), _ptr(pad_mask), B, L, _ptr(kv_cache), _stream(stream))
         _abi.check(st, self.h)
         return kv_cache
@@ -125,10 +136,10 @@ class SmolVLA:
         B, H, A = noise.shape
         L = pad_mask.shape[1]
         if actions is None:
-            actions = torch.empty_like(noise)
+            actions = _new(stream, noise.shape, noise.dtype, noise.device)
         tr = None
         if trace:
-            tr = torch.empty((n_steps, 2, B, H, A), dtype=torch.float32, device=noise.device)
+            tr = _new(stream, (n_steps, 2, B, H, A), torch.float32, noise.device)
         st = self.lib.svla_denoise(self.h, _ptr(kv_cache), _ptr(pad_mask), B, L, _ptr(noise), H, n_steps,
                                    _ptr(actions), _ptr(tr), _stream(stream))
         _abi.check(st, self.h)
@@ -143,10 +154,10 @@ class SmolVLA:
         L = pad_mask.shape[1]
         d = prefix.shape[1]
         if actions is None:
-            actions = torch.empty_like(noise)
+            actions = _new(stream, noise.shape, noise.dtype, noise.device)
         tr = None
         if trace:
-            tr = torch.empty((n_steps, 2, B, H, A), dtype=torch.float32, device=noise.device)
+            tr = _new(stream, (n_steps, 2, B, H, A), torch.float32, noise.device)
         st = self.lib.svla_denoise_prefix(self.h, _ptr(kv_cache), _ptr(pad_mask), B, L, _ptr(noise), H, n_steps,
                                           _ptr(prefix), d, _ptr(actions), _ptr(tr), _stream(stream))
         _abi.check(st, self.h)
@@ -156,9 +167,9 @@ class SmolVLA:
                kv_cache: Optional[torch.Tensor] = None, return_noise: bool = False, stream=None):
         B, L = pad_mask.shape
         if kv_cache is None:
-            kv_cache = self.new_kv_cache(B, L)
-        actions = torch.empty((B, H, self.action_dim), dtype=torch.float32, device=embeds.device)
-        noise = torch.empty_like(actions) if return_noise else None
+            kv_cache = self.new_kv_cache(B, L, stream)
+        actions = _new(stream, (B, H, self.action_dim), torch.float32, embeds.device)
+        noise = _new(stream, actions.shape, torch.float32, embeds.device) if return_noise else None
         st = self.lib.svla_sample(self.h, _ptr(embeds), _ptr(pad_mask), B, L, seed, H, n_steps,
                                   _ptr(kv_cache), _ptr(noise), _ptr(actions), _stream(stream))
         _abi.check(st, self.h)
@@ -187,8 +198,8 @@ class SmolVLA:
         T = text.shape[1]
         grid, r = self.asm
         L = n_img * (grid // r) ** 2 + T + 1
-        embeds = torch.empty((B, L, self.cfg.p_width), dtype=torch.bfloat16, device=vis.device)
-        pad = torch.empty((B, L), dtype=torch.uint8, device=vis.device)
+        embeds = _new(stream, (B, L, self.cfg.p_width), torch.bfloat16, vis.device)
+        pad = _new(stream, (B, L), torch.uint8, vis.device)
         st = self.lib.svla_assemble_prefix(self.h, _ptr(vis), _ptr(text) if T else None,
                                            _ptr(text_valid) if T else None, _ptr(state), B, n_img, T,
                                            _ptr(embeds), _ptr(pad), _stream(stream))
@@ -207,8 +218,8 @@ class SmolVLA:
         L = pad_mask.shape[1]
         n = int(self.lib.svla_train_grad_elems(self.h))
         if grads is None:
-            grads = torch.empty(n, dtype=torch.float32, device=actions.device)
-        loss = torch.empty(1, dtype=torch.float32, device=actions.device)
+            grads = _new(stream, n, torch.float32, actions.device)
+        loss = _new(stream, 1, torch.float32, actions.device)
         st = self.lib.svla_train_step(self.h, _ptr(kv_cache), _ptr(pad_mask), B, L, _ptr(actions), _ptr(noise),
                                       _ptr(t), H, _ptr(loss), _ptr(grads), _stream(stream))
         _abi.check(st, self.h)
@@ -218,9 +229,7 @@ class SmolVLA:
         """The expert and head weights that the next ``train_step`` reads, bf16 in the gradients' order."""
         n = int(self.lib.svla_train_grad_elems(self.h))
         if out is None:
-            out = torch.empty(n, dtype=torch.bfloat16, device=f"cuda:{self.device}")
-            if stream is not None:
-                out.record_stream(stream)
+            out = _new(stream, n, torch.bfloat16, f"cuda:{self.device}")
         _abi.check(self.lib.svla_train_weights(self.h, _vec(out, n, "out", torch.bfloat16, self.device),
                                                _stream(stream)), self.h)
         return out
@@ -310,8 +319,8 @@ def op_quantize_affine8(W: torch.Tensor, stream=None) -> Tuple[torch.Tensor, tor
     G = ceil(K / 64) groups (the last one holds the K mod 64 remaining inputs when K % 64 != 0)."""
     lib = _abi.load()
     N, K = W.shape
-    q = torch.empty((N, K), dtype=torch.uint8, device=W.device)
-    ab = torch.empty(((K + 63) // 64, N, 2), dtype=torch.bfloat16, device=W.device)
+    q = _new(stream, (N, K), torch.uint8, W.device)
+    ab = _new(stream, ((K + 63) // 64, N, 2), torch.bfloat16, W.device)
     _abi.check(lib.svla_op_quantize_affine8(_ptr(W), W.stride(0), N, K, _ptr(q), q.stride(0), _ptr(ab),
                                             _stream(stream)))
     return q, ab
