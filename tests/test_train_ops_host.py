@@ -295,3 +295,28 @@ def test_outputs_come_from_the_pool_of_the_stream_that_writes_them(given_stream,
         call()
         assert [s for _, s in made] == [stream] * n and told == ["current"] * n
     m.h = None
+
+
+def test_handle_calls_take_the_current_stream_of_the_handles_device(monkeypatch):
+    """Whatever the current device: another device's stream does not order the handle's work."""
+    torch = pytest.importorskip("torch")
+    import types
+    from vision_language_action_b200 import runtime as rt
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(cuda_stream=(device, "s")))
+    monkeypatch.setattr(ctypes, "c_void_p", lambda x: x)
+    monkeypatch.setattr(rt, "_ptr", lambda t: None if t is None else 8)
+    monkeypatch.setattr(rt, "_vec", lambda *a: 8)
+    monkeypatch.setattr(rt, "_new", lambda stream, shape, dtype, device: torch.empty(shape, dtype=dtype))
+    lib = AnyLib()
+    m = handle_without_gpu(rt, lib)
+    m.device = 3
+    z = torch.ones
+    f, pad, kv = z(2, 3, 8), z(2, 5), z(4)
+    for call in (lambda: m.prefill(f, pad), lambda: m.denoise(kv, pad, f, 4),
+                 lambda: m.denoise_prefix(kv, pad, f, 4, z(2, 1, 8)), lambda: m.sample(f, pad, 3, 3, 4),
+                 lambda: m.assemble_prefix(z(2, 1, 16, 4), z(2, 5, 6), z(2, 5), z(2, 3)),
+                 lambda: m.train_step(kv, pad, f, f, z(2)), lambda: m.train_weights(),
+                 lambda: m.train_update(f, f, (f, f, None, None), 1), lambda: m.device_status()):
+        call()
+        assert lib.calls[-1][1][-1] == (3, "s"), lib.calls[-1]
+    m.h = None

@@ -36,8 +36,9 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream: Optional[torch.cuda.Stream]):
-    s = stream if stream is not None else torch.cuda.current_stream()
+def _stream(stream: Optional[torch.cuda.Stream], device=None):
+    """The stream given, else the current one of `device` (None: of the current device)."""
+    s = stream if stream is not None else torch.cuda.current_stream(device)
     return ctypes.c_void_p(s.cuda_stream)
 
 
@@ -126,7 +127,8 @@ class SmolVLA:
         B, L = pad_mask.shape
         if kv_cache is None:
             kv_cache = self.new_kv_cache(B, L, stream)
-        st = self.lib.svla_prefill(self.h, _ptr(embeds), _ptr(pad_mask), B, L, _ptr(kv_cache), _stream(stream))
+        st = self.lib.svla_prefill(self.h, _ptr(embeds), _ptr(pad_mask), B, L, _ptr(kv_cache),
+                                   _stream(stream, self.device))
         _abi.check(st, self.h)
         return kv_cache
 
@@ -141,7 +143,7 @@ class SmolVLA:
         if trace:
             tr = _new(stream, (n_steps, 2, B, H, A), torch.float32, noise.device)
         st = self.lib.svla_denoise(self.h, _ptr(kv_cache), _ptr(pad_mask), B, L, _ptr(noise), H, n_steps,
-                                   _ptr(actions), _ptr(tr), _stream(stream))
+                                   _ptr(actions), _ptr(tr), _stream(stream, self.device))
         _abi.check(st, self.h)
         return actions, tr
 
@@ -159,7 +161,7 @@ class SmolVLA:
         if trace:
             tr = _new(stream, (n_steps, 2, B, H, A), torch.float32, noise.device)
         st = self.lib.svla_denoise_prefix(self.h, _ptr(kv_cache), _ptr(pad_mask), B, L, _ptr(noise), H, n_steps,
-                                          _ptr(prefix), d, _ptr(actions), _ptr(tr), _stream(stream))
+                                          _ptr(prefix), d, _ptr(actions), _ptr(tr), _stream(stream, self.device))
         _abi.check(st, self.h)
         return actions, tr
 
@@ -171,7 +173,7 @@ class SmolVLA:
         actions = _new(stream, (B, H, self.action_dim), torch.float32, embeds.device)
         noise = _new(stream, actions.shape, torch.float32, embeds.device) if return_noise else None
         st = self.lib.svla_sample(self.h, _ptr(embeds), _ptr(pad_mask), B, L, seed, H, n_steps,
-                                  _ptr(kv_cache), _ptr(noise), _ptr(actions), _stream(stream))
+                                  _ptr(kv_cache), _ptr(noise), _ptr(actions), _stream(stream, self.device))
         _abi.check(st, self.h)
         return (actions, kv_cache, noise) if return_noise else (actions, kv_cache)
 
@@ -202,7 +204,7 @@ class SmolVLA:
         pad = _new(stream, (B, L), torch.uint8, vis.device)
         st = self.lib.svla_assemble_prefix(self.h, _ptr(vis), _ptr(text) if T else None,
                                            _ptr(text_valid) if T else None, _ptr(state), B, n_img, T,
-                                           _ptr(embeds), _ptr(pad), _stream(stream))
+                                           _ptr(embeds), _ptr(pad), _stream(stream, self.device))
         _abi.check(st, self.h)
         return embeds, pad
 
@@ -221,7 +223,7 @@ class SmolVLA:
             grads = _new(stream, n, torch.float32, actions.device)
         loss = _new(stream, 1, torch.float32, actions.device)
         st = self.lib.svla_train_step(self.h, _ptr(kv_cache), _ptr(pad_mask), B, L, _ptr(actions), _ptr(noise),
-                                      _ptr(t), H, _ptr(loss), _ptr(grads), _stream(stream))
+                                      _ptr(t), H, _ptr(loss), _ptr(grads), _stream(stream, self.device))
         _abi.check(st, self.h)
         return loss, grads
 
@@ -231,7 +233,7 @@ class SmolVLA:
         if out is None:
             out = _new(stream, n, torch.bfloat16, f"cuda:{self.device}")
         _abi.check(self.lib.svla_train_weights(self.h, _vec(out, n, "out", torch.bfloat16, self.device),
-                                               _stream(stream)), self.h)
+                                               _stream(stream, self.device)), self.h)
         return out
 
     def new_moments(self, state_bits: int = 32):
@@ -267,7 +269,7 @@ class SmolVLA:
             _vec(m, n, "m", kinds[0], dev), _vec(v, n, "v", kinds[1], dev),
             _vec(ms, k, "m_scale", f32, dev) if bits == 8 else None,
             _vec(vs, k, "v_scale", f32, dev) if bits == 8 else None, ctypes.byref(a),
-            _vec(grad_norm, 1, "grad_norm", f32, dev), _stream(stream))
+            _vec(grad_norm, 1, "grad_norm", f32, dev), _stream(stream, self.device))
         _abi.check(st, self.h)
 
     def set_prefix_weights(self, bits: int) -> None:
@@ -291,7 +293,7 @@ class SmolVLA:
 
     def device_status(self, stream=None) -> int:
         """Synchronise the stream; return (and clear) the device-side status."""
-        return int(self.lib.svla_device_status(self.h, _stream(stream)))
+        return int(self.lib.svla_device_status(self.h, _stream(stream, self.device)))
 
 
 # ----------------------------------------------------------------------
