@@ -683,3 +683,24 @@ def test_a_first_moment_near_the_end_of_float32(exponent):
         codes, s = oo.encode(x, u, fmt, keep)
         assert np.array_equal(scale.cpu().numpy(), s)
         assert np.array_equal(codes_of(got), codes)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_the_first_step_on_another_stream_beside_queued_work(bits):
+    """The moments' zeros, the norm and the workspace are made on the stream current at construction, behind what is
+    queued there; the first step runs on another."""
+    n = 300_000
+    g = torch.randn(n, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)) * 1e-3
+    ref, p = torch.ones(n, device=DEV), torch.ones(n, device=DEV)
+    kw = dict(lr=1e-2, state_bits=bits, max_norm=0.1, capturable=True)
+    AdamW([ref], **kw).step([g])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)  # about 10 ms
+    tmp = torch.empty(8 * n, dtype=torch.uint8, device=DEV).fill_(255)
+    del tmp
+    opt = AdamW([p], **kw)
+    assert torch.cuda.current_stream().query()
+    opt.step([g], stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(p, ref) and int(opt.step_tensor) == 1

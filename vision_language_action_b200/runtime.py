@@ -475,7 +475,9 @@ class AdamW:
     tensors (the scales None with 32 bits), resumes with those moments and ``step`` with that many steps taken.
     ``capturable`` counts the steps on the device, so that a captured ``step`` counts on at every replay; ``lr``
     may then be a float64 CUDA tensor of one element, read at every step. A step without it that is captured repeats
-    its own step number at every replay. Autograd does not see the parameters change: step between a backward pass and
+    its own step number at every replay. The constructor waits for the stream that is current then, so that the first step
+    may run on any other (the tensors given are the caller's to order, and so are steps on different streams).
+    Autograd does not see the parameters change: step between a backward pass and
     the next forward, not between a forward and its backward pass.
     """
 
@@ -547,6 +549,10 @@ class AdamW:
         self._args_ref, self._ws_bytes = ctypes.byref(a), ws
         self._ws_ptr = self._ws.data_ptr() if ws else None
         self._norm_ptr = self.grad_norm.data_ptr() if max_norm else None
+        # the memory made here is zero, and free of its former use, on this stream alone: the first step may run on another
+        with torch.cuda.device(self._dev):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
 
     @staticmethod
     def _check(ts, sizes, dtype, dev: int, what: str, none_too: bool = False) -> None:
