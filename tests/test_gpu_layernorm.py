@@ -398,3 +398,37 @@ def test_workspaces_on_a_given_stream_beside_queued_work():
         torch.cuda.synchronize()
         assert [int(k) for k in kept] == [n * k for k in range(1, 40)]
     assert all(torch.equal(x, y) for x, y in zip((a["dx"], a["dgamma"], a["dbeta"], out), want))
+
+
+@pytest.mark.parametrize("widths", [(768, 12288), (6400, 8192)])
+def test_two_threads_with_two_widths_of_one_kernel(widths):
+    """Widths that share a kernel and differ in the shared memory that it takes, in two threads at once: every call
+    launches and gives what it gives alone."""
+    import threading
+    calls, errors, outs = 4000, [], {}
+    start = threading.Barrier(2)
+
+    def work(D, stream):
+        try:
+            with torch.cuda.stream(stream):
+                a = make(9, D, x="bf16", y="bf16", seed=1)
+                op_layernorm(a["x"], a["gamma"], a["beta"], a["y"], 1e-5, a["mean"], a["rstd"])
+                start.wait(60)
+                for _ in range(calls):
+                    op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"], a["rstd"], a["dx"], a["dgamma"], a["dbeta"])
+                stream.synchronize()
+                outs[D] = a
+        except Exception as e:  # noqa: BLE001
+            errors.append(f"{D}: {e}")
+
+    threads = [threading.Thread(target=work, args=(D, torch.cuda.Stream())) for D in widths]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for D in widths:
+        a = outs[D]
+        want = make(9, D, x="bf16", y="bf16", seed=1)
+        op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"], a["rstd"], want["dx"], want["dgamma"], want["dbeta"])
+        assert all(torch.equal(a[k], want[k]) for k in ("dx", "dgamma", "dbeta"))

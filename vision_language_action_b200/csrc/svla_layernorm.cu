@@ -627,6 +627,20 @@ cudaError_t resident_per_sm(LnFn fn, int slot, int threads, size_t smem, int* bl
   return cudaSuccess;
 }
 
+// Shared memory that the backward's kernel of NU units may take: the column sums of rows on 512 threads (more, narrower
+// rows a block take less). The limit is set once a kernel and device, to this: set to each call's own size, a call of
+// another thread could lower it before the launch.
+constexpr int ln_bwd_smem_max(int NU) { return 2 * NU * 8 * 512 * (int)sizeof(float); }
+cudaError_t allow_bwd_smem(LnFn fn, int slot, int NU) {
+  static std::atomic<bool> done[8 * 3 * 17 * 4][64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[slot][dev].load())) return e;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, ln_bwd_smem_max(NU));
+  if (e == cudaSuccess && dev < 64) done[slot][dev].store(true);
+  return e;
+}
+
 svla_status run(LnArgs& a, int xt, int yt, int wt, bool bwd, bool vec, cudaStream_t s) {
   const LnPlan p = bwd ? ln_bwd_plan(a.D) : ln_fwd_plan(a.D, vec, xt == SVLA_TYPE_BF16);
   a.T = p.T;
@@ -638,11 +652,12 @@ svla_status run(LnArgs& a, int xt, int yt, int wt, bool bwd, bool vec, cudaStrea
   const size_t smem = p.smem_acc || a.dgamma || a.dbeta ? full : 0;
   int blocks = (a.M - 1) / p.R + 1;
   cudaError_t e = cudaSuccess;
-  if (full > 40 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)full);
+  const int kind = (xt == SVLA_TYPE_BF16 ? 4 : 0) | (yt == SVLA_TYPE_BF16 ? 2 : 0) | (wt == SVLA_TYPE_BF16 ? 1 : 0);
+  const int slot = ((kind * 3 + step) * 17 + p.T / 32) * 4 + p.NU - 1;
+  if (full > 40 * 1024) e = allow_bwd_smem(fn, slot, p.NU);
   if (e == cudaSuccess && bwd && blocks > 1) {
     int per_sm = 0;
-    const int kind = (xt == SVLA_TYPE_BF16 ? 4 : 0) | (yt == SVLA_TYPE_BF16 ? 2 : 0) | (wt == SVLA_TYPE_BF16 ? 1 : 0);
-    e = resident_per_sm(fn, ((kind * 3 + step) * 17 + p.T / 32) * 4 + p.NU - 1, p.threads, full, &per_sm);
+    e = resident_per_sm(fn, slot, p.threads, full, &per_sm);
     if (e == cudaSuccess) blocks = ln_bwd_blocks(a.M, p, per_sm);
   }
   a.cluster = bwd && blocks > 1 && blocks <= LN_CLUSTER && (a.dgamma || a.dbeta);
