@@ -536,7 +536,8 @@ def gemm_roofline(s, B, L, H, n_steps, dev, hbm_peak):
     def run(plans):
         st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
         for epi, A, W, C, M, N, K in plans:
-            _abi.check(lib.svla_op_gemm(epi, P(A), K, P(W), K, M, N, K, P(C), N, None, 0, None, 0, None, st))
+            _abi.check(lib.svla_op_gemm(epi | _abi.GEMM_W_READY, P(A), K, P(W), K, M, N, K, P(C), N, None, 0, None, 0,
+                                        None, st))
 
     def graph_time(plans, reps=10):
         cs = torch.cuda.Stream()

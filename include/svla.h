@@ -367,6 +367,10 @@ SVLA_API const char* svla_status_string(svla_status s);
 #define SVLA_EPI_BF16       1   /* C(bf16) = acc (+ bias)                     */
 #define SVLA_EPI_ADD_F32    2   /* C(f32) += acc (+ bias)    (residual add)   */
 #define SVLA_EPI_SILU_BF16  3   /* C(bf16) = silu(acc + bias)                 */
+/* Or'ed to the epilogue of svla_op_gemm: nothing that may still be unfinished
+ * in the stream writes W, so its first tiles may be fetched while the call
+ * before drains (a chain of products on weights that stay as they are). */
+#define SVLA_GEMM_W_READY   0x100
 
 /* C[M, N] = A[M, K] · W[N, K]^T on the tcgen05 tensor cores, bf16 inputs,
  * fp32 accumulation (the projections of every layer: "noeira docs, SmolVLA"
@@ -381,7 +385,9 @@ SVLA_API const char* svla_status_string(svla_status s);
  *   every call) and the last CTA of each tile sums them in fixed order, so the
  *   result is bitwise deterministic.
  *   status: device int, set (first error wins) to SVLA_ERR_TIMEOUT if a
- *   bounded wait ran out; may be NULL. */
+ *   bounded wait ran out; may be NULL.
+ *   W may be what an earlier call on the stream writes, the one just before
+ *   among them (unless SVLA_GEMM_W_READY is given). */
 SVLA_API svla_status svla_op_gemm(int epilogue, const void* A, int lda, const void* W, int ldw,
                          int M, int N, int K, void* C, int ldc, const float* bias,
                          int splits, void* workspace, size_t workspace_bytes,

@@ -21,6 +21,7 @@ SVLA_ERR_TIMEOUT, SVLA_ERR_UNSUPPORTED = -7, -8
 
 TYPE_F32, TYPE_BF16 = 0, 1
 EPI_F32, EPI_BF16, EPI_ADD_F32, EPI_SILU_BF16 = 0, 1, 2, 3
+GEMM_W_READY = 0x100
 
 
 class SvlaConfig(ctypes.Structure):

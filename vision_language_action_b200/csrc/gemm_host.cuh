@@ -439,7 +439,7 @@ inline GemmPlan plan_gemm_w8(int M, int N, int K, int forced_splits, int min_bn 
 template <int BN, int ST, int EPI>
 inline cudaError_t launch_w8_inst(const CUtensorMap& ta, const CUtensorMap& tq, const CUtensorMap& ts,
                                   const GemmArgs& args, const uint16_t* gain, dim3 grid, int cluster_z,
-                                  cudaStream_t s) {
+                                  cudaStream_t s, bool pdl) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(GEMM_THREADS);
@@ -448,7 +448,7 @@ inline cudaError_t launch_w8_inst(const CUtensorMap& ta, const CUtensorMap& tq, 
   cudaLaunchAttribute at[2];
   int n = 0;
   at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[n].val.programmaticStreamSerializationAllowed = 1;
+  at[n].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   ++n;
   if (cluster_z > 1) {
     at[n].id = cudaLaunchAttributeClusterDimension;
@@ -464,17 +464,17 @@ inline cudaError_t launch_w8_inst(const CUtensorMap& ta, const CUtensorMap& tq, 
 
 template <int BN, int ST>
 inline cudaError_t dispatch_w8(int epi, const CUtensorMap& ta, const CUtensorMap& tq, const CUtensorMap& ts,
-                               const GemmArgs& a, const uint16_t* gain, dim3 g, int cz, cudaStream_t s) {
+                               const GemmArgs& a, const uint16_t* gain, dim3 g, int cz, cudaStream_t s, bool pdl) {
   switch (epi) {
-    case GE_F32: return launch_w8_inst<BN, ST, GE_F32>(ta, tq, ts, a, gain, g, cz, s);
-    case GE_BF16: return launch_w8_inst<BN, ST, GE_BF16>(ta, tq, ts, a, gain, g, cz, s);
-    case GE_ADD_F32: return launch_w8_inst<BN, ST, GE_ADD_F32>(ta, tq, ts, a, gain, g, cz, s);
-    case GE_SILU_BF16: return launch_w8_inst<BN, ST, GE_SILU_BF16>(ta, tq, ts, a, gain, g, cz, s);
-    case GE_QKV_ROPE32: return launch_w8_inst<BN, ST, GE_QKV_ROPE32>(ta, tq, ts, a, gain, g, cz, s);
+    case GE_F32: return launch_w8_inst<BN, ST, GE_F32>(ta, tq, ts, a, gain, g, cz, s, pdl);
+    case GE_BF16: return launch_w8_inst<BN, ST, GE_BF16>(ta, tq, ts, a, gain, g, cz, s, pdl);
+    case GE_ADD_F32: return launch_w8_inst<BN, ST, GE_ADD_F32>(ta, tq, ts, a, gain, g, cz, s, pdl);
+    case GE_SILU_BF16: return launch_w8_inst<BN, ST, GE_SILU_BF16>(ta, tq, ts, a, gain, g, cz, s, pdl);
+    case GE_QKV_ROPE32: return launch_w8_inst<BN, ST, GE_QKV_ROPE32>(ta, tq, ts, a, gain, g, cz, s, pdl);
   }
   if constexpr (BN % 64 == 0) {
-    if (epi == GE_SWIGLU) return launch_w8_inst<BN, ST, GE_SWIGLU>(ta, tq, ts, a, gain, g, cz, s);
-    if (epi == GE_QKV_ROPE64) return launch_w8_inst<BN, ST, GE_QKV_ROPE64>(ta, tq, ts, a, gain, g, cz, s);
+    if (epi == GE_SWIGLU) return launch_w8_inst<BN, ST, GE_SWIGLU>(ta, tq, ts, a, gain, g, cz, s, pdl);
+    if (epi == GE_QKV_ROPE64) return launch_w8_inst<BN, ST, GE_QKV_ROPE64>(ta, tq, ts, a, gain, g, cz, s, pdl);
   }
   return cudaErrorInvalidValue;
 }
@@ -501,10 +501,10 @@ inline cudaError_t set_attrs_w8() {
 
 // Full launch of the int8 GEMM. Q: codes [N, K] (row stride ldq bytes); ab:
 // (alpha, beta) pairs [ceil(K/64)][N][2]; gain: bf16 [K] or null. K % 16 == 0
-// and N % 4 == 0 (TMA strides), checked by the callers.
+// and N % 4 == 0 (TMA strides), checked by the callers. pdl as in run_gemm.
 inline cudaError_t run_gemm_w8(int epi, const void* A, int lda, const uint8_t* Q, size_t ldq, const uint16_t* ab,
                                const uint16_t* gain, int M, int N, int K, GemmArgs args, const GemmPlan& p,
-                               cudaStream_t s) {
+                               cudaStream_t s, bool pdl) {
   CUtensorMap ta, tq, ts;
   if (!make_tmap_bf16(&ta, A, M, K, lda, GEMM_BM)) return cudaErrorInvalidValue;
   if (!make_tmap_u8(&tq, Q, N, K, ldq, p.bn)) return cudaErrorInvalidValue;
@@ -517,9 +517,9 @@ inline cudaError_t run_gemm_w8(int epi, const void* A, int lda, const uint8_t* Q
   args.red_mode = p.red;
   const dim3 grid(p.n_tiles, p.m_tiles, p.splits);
   const int cz = p.red == GEMM_RED_CLUSTER ? p.splits : 1;
-  if (p.bn == 32 && p.stages == 5) return dispatch_w8<32, 5>(epi, ta, tq, ts, args, gain, grid, cz, s);
-  if (p.bn == 64 && p.stages == 4) return dispatch_w8<64, 4>(epi, ta, tq, ts, args, gain, grid, cz, s);
-  if (p.bn == 128 && p.stages == 4) return dispatch_w8<128, 4>(epi, ta, tq, ts, args, gain, grid, cz, s);
+  if (p.bn == 32 && p.stages == 5) return dispatch_w8<32, 5>(epi, ta, tq, ts, args, gain, grid, cz, s, pdl);
+  if (p.bn == 64 && p.stages == 4) return dispatch_w8<64, 4>(epi, ta, tq, ts, args, gain, grid, cz, s, pdl);
+  if (p.bn == 128 && p.stages == 4) return dispatch_w8<128, 4>(epi, ta, tq, ts, args, gain, grid, cz, s, pdl);
   return cudaErrorInvalidValue;
 }
 

@@ -414,11 +414,11 @@ void free_all(svla_handle* h) {
   h->cap = nullptr;
 }
 
-// Launch with programmatic stream serialization: the kernel may start while its
-// predecessor drains; it touches activations only after griddep_wait().
+// Launch, with pdl by programmatic stream serialization: the kernel may start
+// while its predecessor drains; it touches activations only after griddep_wait().
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                       Args&&... args) {
+cudaError_t launch(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                   Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -426,10 +426,15 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                       Args&&... args) {
+  return launch(true, kernel, grid, block, smem, s, std::forward<Args>(args)...);
 }
 
 // one GEMM of the schedule
@@ -462,7 +467,7 @@ cudaError_t gemm8(svla_handle* h, int epi, const bf16* A, int lda, const uint8_t
   GemmPlan p = plan_gemm_w8(M, w.N, w.K, 0, gemm_min_bn(epi));
   args.status = h->status;
   args.wait_ns = g_wait_ns.load();
-  return run_gemm_w8(epi, A, lda, q, (size_t)w.K, ab, gain, M, w.N, w.K, args, p, s);
+  return run_gemm_w8(epi, A, lda, q, (size_t)w.K, ab, gain, M, w.N, w.K, args, p, s, /*pdl=*/true);
 }
 
 GemmArgs out_args(void* out, int ldo, const float* bias = nullptr) {
@@ -475,10 +480,10 @@ GemmArgs out_args(void* out, int ldo, const float* bias = nullptr) {
 }
 
 cudaError_t rmsnorm(const void* x, bool x_bf16, float* x_copy, const bf16* g, int M, int D, float eps, bf16* y,
-                    cudaStream_t s) {
+                    cudaStream_t s, bool pdl = true) {
   const int blocks = (M + 7) / 8;
-  if (x_bf16) return launch_pdl(rmsnorm_kernel<true>, dim3(blocks), dim3(256), 0, s, x, x_copy, g, M, D, eps, y);
-  return launch_pdl(rmsnorm_kernel<false>, dim3(blocks), dim3(256), 0, s, x, (float*)nullptr, g, M, D, eps, y);
+  if (x_bf16) return launch(pdl, rmsnorm_kernel<true>, dim3(blocks), dim3(256), 0, s, x, x_copy, g, M, D, eps, y);
+  return launch(pdl, rmsnorm_kernel<false>, dim3(blocks), dim3(256), 0, s, x, (float*)nullptr, g, M, D, eps, y);
 }
 
 cudaError_t attention(const bf16* q, int ldq, const bf16* k, const bf16* v, int ldkv, const uint8_t* valid, int B,
@@ -1903,6 +1908,9 @@ svla_status svla_device_status(svla_handle* h, void* stream) {
 }
 
 // ---- kernel-level entry points ---------------------------------------------
+// The kernels that fetch weights before their dependency wait are launched here
+// behind all earlier work of the stream (pdl = false): a caller's W, codes or
+// gains may be what the call before writes.
 static int epi_code(int epi) {
   switch (epi) {
     case SVLA_EPI_F32: return GE_F32;
@@ -1939,7 +1947,8 @@ size_t svla_op_gemm_workspace_bytes(int M, int N, int K, int splits) {
 svla_status svla_op_gemm(int epilogue, const void* A, int lda, const void* W, int ldw, int M, int N, int K, void* C,
                          int ldc, const float* bias, int splits, void* workspace, size_t workspace_bytes, int* status,
                          void* stream) {
-  const int epi = epi_code(epilogue);
+  const bool w_ready = epilogue >= 0 && (epilogue & SVLA_GEMM_W_READY);
+  const int epi = epi_code(w_ready ? epilogue & ~SVLA_GEMM_W_READY : epilogue);
   if (epi < 0) return fail(nullptr, SVLA_ERR_ARG, "unknown epilogue");
   if (!A || !W || !C) return fail(nullptr, SVLA_ERR_ARG, "null pointer");
   if (M < 1 || N < 1 || K < 1 || splits < 0 || lda < K || ldw < K || ldc < N || lda % 8 || ldw % 8 ||
@@ -1962,7 +1971,8 @@ svla_status svla_op_gemm(int epilogue, const void* A, int lda, const void* W, in
   GemmArgs a = out_args(C, ldc, bias);
   a.status = status;
   a.wait_ns = g_wait_ns.load();
-  cudaError_t e = run_gemm(epi, A, lda, W, ldw, M, N, K, a, p, part, cnt, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = run_gemm(epi, A, lda, W, ldw, M, N, K, a, p, part, cnt, reinterpret_cast<cudaStream_t>(stream),
+                           /*pdl=*/w_ready);
   if (e != cudaSuccess) return cuda_fail(nullptr, e, "gemm launch");
   return SVLA_OK;
 }
@@ -2012,7 +2022,7 @@ svla_status svla_op_gemm_w8(int epilogue, const void* A, int lda, const void* q,
   a.wait_ns = g_wait_ns.load();
   cudaError_t e = run_gemm_w8(epi, A, lda, reinterpret_cast<const uint8_t*>(q), (size_t)ldq,
                               reinterpret_cast<const uint16_t*>(ab), reinterpret_cast<const uint16_t*>(gain), M, N, K,
-                              a, p, reinterpret_cast<cudaStream_t>(stream));
+                              a, p, reinterpret_cast<cudaStream_t>(stream), /*pdl=*/false);
   if (e != cudaSuccess) return cuda_fail(nullptr, e, "gemm_w8 launch");
   return SVLA_OK;
 }
@@ -2040,7 +2050,7 @@ svla_status svla_op_rmsnorm(const float* x, const void* g, int M, int D, float e
   if (!x || !g || !y) return fail(nullptr, SVLA_ERR_ARG, "null pointer");
   if (M < 1 || D < 4 || D % 4 || D > 2048 || !(eps > 0.f)) return fail(nullptr, SVLA_ERR_SHAPE, "bad sizes");
   cudaError_t e = rmsnorm(x, false, nullptr, reinterpret_cast<const bf16*>(g), M, D, eps, reinterpret_cast<bf16*>(y),
-                          reinterpret_cast<cudaStream_t>(stream));
+                          reinterpret_cast<cudaStream_t>(stream), /*pdl=*/false);
   if (e != cudaSuccess) return cuda_fail(nullptr, e, "rmsnorm launch");
   return SVLA_OK;
 }

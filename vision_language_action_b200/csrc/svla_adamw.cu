@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(ADAMW_THREADS, BITS == 8 && sizeof(TP) == 2 ? 
   __shared__ float s_clip;
   __shared__ float s_coef[3];
   __shared__ __align__(16) uint16_t rnd[BITS == 8 ? ADAMW_WARPS : 1][ADAMW_BLOCK];
-  // no early launch of dependents: what is written here may be a weight, which other kernels fetch before their wait
+  // no early launch of dependents: what is written here may be a weight, which kernels fetch before their wait
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float clip = 1.f, keep_all = c.keep, step_size = c.step_size, isb2 = c.isb2;

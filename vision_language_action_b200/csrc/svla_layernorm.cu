@@ -250,7 +250,7 @@ struct Moments {
 template <typename TX, typename TY, typename TW, int NU, int STEP>
 __global__ void __launch_bounds__(NU <= 2 ? 1024 : 512) layernorm_kernel(const LnArgs a) {
   __shared__ Moments red[32];
-  // no early launch of dependents: y may be the W of the GEMM that follows, which fetches it before its wait
+  // no early launch of dependents: y may be a weight of what follows, and kernels fetch weights before their wait
   griddep_wait();  // nothing is read before: the weights may come from an optimiser step
   const int T = a.T, tid = threadIdx.x % T, D = a.D;
   const long long row = (long long)blockIdx.x * (blockDim.x / T) + threadIdx.x / T;
