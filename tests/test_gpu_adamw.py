@@ -704,3 +704,33 @@ def test_the_first_step_on_another_stream_beside_queued_work(bits):
     opt.step([g], stream=side)
     torch.cuda.synchronize()
     assert torch.equal(p, ref) and int(opt.step_tensor) == 1
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("step", [3, 2 ** 32, 2 ** 32 + 1, 2 ** 53 - 1])
+def test_a_device_learning_rate_beside_the_hosts_step(step, bits):
+    """lr_device without step_device: the bias corrections are those of the whole step number, as with a host's rate."""
+    lib, n = _abi.load(), 3000
+    outs = []
+    for on_device in (False, True):
+        st = make([n], bits=bits, seed=12)
+        t, a = _abi.SvlaAdamwTensor(), _abi.SvlaAdamwArgs()
+        t.param, t.grad, t.m, t.v = (st[k][0].data_ptr() for k in ("p", "g", "m", "v"))
+        if bits == 8:
+            t.m_scale, t.v_scale = st["ms"][0].data_ptr(), st["vs"][0].data_ptr()
+        t.n, t.decay = n, 1
+        lr = torch.full((1,), 1e-2, dtype=torch.float64, device=DEV)
+        a.state_bits, a.lr, a.beta1, a.beta2, a.eps, a.weight_decay, a.step = bits, 1e-2, 0.9, 0.999, 1e-8, 0.1, step
+        if on_device:
+            a.lr, a.lr_device = 0.0, lr.data_ptr()
+        _abi.check(lib.svla_op_adamw(ctypes.byref(t), 1, ctypes.byref(a), None, 0, None,
+                                     torch.cuda.current_stream().cuda_stream))
+        torch.cuda.synchronize()
+        outs.append(st)
+    host, dev = outs
+    for k in ("m", "v"):
+        assert torch.equal(host[k][0].view(torch.uint8), dev[k][0].view(torch.uint8))
+    # the three coefficients may differ by a unit of either side's arithmetic: two units of the step, which is no larger
+    # than |p0| + |p|, and one of p0 (1 - lr wd); p itself is rounded on both sides: 3 |p0| + 4 |p| units
+    p0, p, q = make([n], bits=bits, seed=12)["p"][0].double(), host["p"][0].double(), dev["p"][0].double()
+    assert torch.isfinite(q).all() and ((p - q).abs() <= 4 * U * (p0.abs() + p.abs())).all()

@@ -85,7 +85,8 @@ struct AdamwCoefs {
   float step_size;  // lr / (1 - b1^t)
   float isb2;       // 1 / sqrt(1 - b2^t)
   double max_norm;  // 0: no clip
-  uint32_t step, tensor0;
+  uint32_t step, tensor0;  // the random bits' counter takes the low word of the step number
+  double t;                // the bias corrections the whole of it
   // read on the device instead of the host's numbers, where given
   const long long* step_dev;
   const double* lr_dev;
@@ -561,7 +562,7 @@ __global__ void __launch_bounds__(ADAMW_THREADS, BITS == 8 && sizeof(TP) == 2 ? 
   uint32_t step = c.step;
   if (c.step_dev || c.lr_dev) {
     if (threadIdx.x == 0) {
-      const double t = c.step_dev ? (double)*c.step_dev : (double)c.step;
+      const double t = c.step_dev ? (double)*c.step_dev : c.t;
       const double lr = c.lr_dev ? *c.lr_dev : c.lr;
       s_coef[0] = (float)(1.0 - lr * c.wd);
       s_coef[1] = (float)(lr / (1.0 - pow(c.beta1, t)));
@@ -853,6 +854,7 @@ svla_status adamw_checked(const svla_adamw_tensor* ts, int n, const svla_adamw_a
   }
   c.max_norm = a->max_norm;
   c.step = (uint32_t)a->step;
+  c.t = (double)a->step;
   c.step_dev = reinterpret_cast<const long long*>(a->step_device);
   c.lr_dev = a->lr_device;
   c.lr = a->lr;
