@@ -320,3 +320,23 @@ def test_handle_calls_take_the_current_stream_of_the_handles_device(monkeypatch)
         call()
         assert lib.calls[-1][1][-1] == (3, "s"), lib.calls[-1]
     m.h = None
+
+
+def test_adamw_scalars_on_the_device():
+    """grad_norm, step_device and lr_device: aligned to their types, and none in memory that the step writes."""
+    a, room = tensor(), BASE - 4096 * 16
+    need = _abi.load().svla_op_adamw_workspace_bytes(1)
+    for bad in (1, 2, 3):
+        st, msg = adamw([a], args(max_norm=1.0), room, need, room - 64 + bad)
+        assert st == ARG and "aligned" in msg
+    for bad in (4, 1):
+        for kw in (dict(step_device=room - 128 + bad), dict(lr_device=room - 128 + bad)):
+            st, msg = adamw([a], args(**kw))
+            assert st == ARG and "aligned" in msg
+    for inside in (a.param, a.m + 8, a.v, a.copy):
+        for kw in (dict(step_device=inside), dict(lr_device=inside)):
+            st, msg = adamw([a], args(**kw))
+            assert st == ARG and "overlaps" in msg
+    for kw in (dict(step_device=room), dict(lr_device=room + need - 8), dict(lr_device=room - 64)):
+        st, msg = adamw([a], args(max_norm=1.0, **kw), room, need, room - 60)
+        assert st == ARG and "overlaps" in msg

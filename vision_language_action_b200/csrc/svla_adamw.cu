@@ -758,7 +758,8 @@ svla_status adamw_launches(const svla_adamw_tensor* ts, int n, const svla_adamw_
 }
 
 svla_status bad(svla_status s, int i, const char* why) {
-  return svla_internal_fail(s, ((i < 0 ? std::string("workspace or grad_norm") : "tensor " + std::to_string(i)) + ": " + why).c_str());
+  return svla_internal_fail(s, ((i < 0 ? std::string("workspace, grad_norm, step_device or lr_device")
+                                       : "tensor " + std::to_string(i)) + ": " + why).c_str());
 }
 
 svla_status adamw_checked(const svla_adamw_tensor* ts, int n, const svla_adamw_args* a, void* workspace,
@@ -781,6 +782,8 @@ svla_status adamw_checked(const svla_adamw_tensor* ts, int n, const svla_adamw_a
       return svla_internal_fail(SVLA_ERR_ARG, "the clip needs a workspace of svla_op_adamw_workspace_bytes(n_tensors)");
     if ((uintptr_t)workspace & 7) return svla_internal_fail(SVLA_ERR_ARG, "the workspace must be 8-byte aligned");
   }
+  if ((clip && (uintptr_t)grad_norm & 3) || ((uintptr_t)a->step_device | (uintptr_t)a->lr_device) & 7)
+    return bad(SVLA_ERR_ARG, -1, "a pointer is not aligned to its element type");
   // every written range must be apart from every other range
   struct Range {
     uintptr_t at, end;
@@ -788,7 +791,7 @@ svla_status adamw_checked(const svla_adamw_tensor* ts, int n, const svla_adamw_a
     bool written;
   };
   std::vector<Range> ranges;
-  ranges.reserve((size_t)n * 7 + 2);
+  ranges.reserve((size_t)n * 7 + 4);
   for (int i = 0; i < n; ++i) {
     const svla_adamw_tensor& t = ts[i];
     if (t.n < 0) return bad(SVLA_ERR_SHAPE, i, "negative size");
@@ -815,6 +818,8 @@ svla_status adamw_checked(const svla_adamw_tensor* ts, int n, const svla_adamw_a
   }
   if (clip) ranges.push_back(Range{(uintptr_t)workspace, (uintptr_t)workspace + svla_op_adamw_workspace_bytes(n), -1, true});
   if (clip && grad_norm) ranges.push_back(Range{(uintptr_t)grad_norm, (uintptr_t)grad_norm + 4, -1, true});
+  if (a->step_device) ranges.push_back(Range{(uintptr_t)a->step_device, (uintptr_t)a->step_device + 8, -1, false});
+  if (a->lr_device) ranges.push_back(Range{(uintptr_t)a->lr_device, (uintptr_t)a->lr_device + 8, -1, false});
   std::sort(ranges.begin(), ranges.end(), [](const Range& x, const Range& y) { return x.at < y.at; });
   uintptr_t end_written = 0, end_any = 0;
   for (const Range& r : ranges) {
