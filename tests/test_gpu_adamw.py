@@ -734,3 +734,33 @@ def test_a_device_learning_rate_beside_the_hosts_step(step, bits):
     # than |p0| + |p|, and one of p0 (1 - lr wd); p itself is rounded on both sides: 3 |p0| + 4 |p| units
     p0, p, q = make([n], bits=bits, seed=12)["p"][0].double(), host["p"][0].double(), dev["p"][0].double()
     assert torch.isfinite(q).all() and ((p - q).abs() <= 4 * U * (p0.abs() + p.abs())).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_moments_stay_where_they_were_at_construction(bits):
+    """A moment given other storage, or dropped from its list: the steps go on with the memory of the construction,
+    which is not given back, and what is allocated since then keeps its values."""
+    n = 300_000
+    a, b = make([n], bits=bits, seed=3), make([n], bits=bits, seed=3)
+    ref = AdamW(a["p"], state_bits=bits, state=(a["m"], a["v"], a["ms"], a["vs"]))
+    opt = AdamW(b["p"], state_bits=bits, state=(b["m"], b["v"], b["ms"], b["vs"]))
+    p = b["p"]
+    # parts of one buffer each: tensors of their own from here on
+    columns = [opt.m, opt.v] + ([opt.m_scale, opt.v_scale] if bits == 8 else [])
+    for c in columns:
+        c[0] = c[0].clone()
+    own = AdamW(p, state_bits=bits, state=(opt.m, opt.v, opt.m_scale, opt.v_scale))
+    size = [c[0].numel() * c[0].element_size() for c in columns]
+    b = opt = None
+    for k, c in enumerate((own.m, own.v) + ((own.m_scale, own.v_scale) if bits == 8 else ())):
+        if k % 2:
+            c[0].data = torch.zeros_like(c[0])
+        else:
+            c[0] = torch.zeros_like(c[0])
+        columns[k] = None
+    fresh = [torch.full((s,), 7, dtype=torch.uint8, device=DEV) for s in size]
+    for _ in range(3):
+        ref.step(a["g"])
+        own.step(a["g"])
+    torch.cuda.synchronize()
+    assert torch.equal(p[0], a["p"][0]) and all((t == 7).all() for t in fresh)

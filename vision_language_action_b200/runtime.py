@@ -472,7 +472,9 @@ class AdamW:
     gradients (left in ``grad_norm``, float32 [1], by every step; a step whose norm is not finite changes nothing
     else, but counts). ``copies`` (bfloat16, one a parameter) receive the updated parameters rounded. ``decay`` says for each
     parameter whether ``weight_decay`` applies (default: to all). ``state`` = (m, v, m_scale, v_scale), lists of
-    tensors (the scales None with 32 bits), resumes with those moments and ``step`` with that many steps taken.
+    tensors (the scales None with 32 bits), resumes with those moments and ``step`` with that many steps taken. The
+    moments stay where they are at construction: load others with ``copy_`` into ``m``, ``v`` and their scales
+    (parameters and copies are followed to storage that they are given).
     ``capturable`` counts the steps on the device, so that a captured ``step`` counts on at every replay; ``lr``
     may then be a float64 CUDA tensor of one element, read at every step. A step without it that is captured repeats
     its own step number at every replay. The constructor waits for the stream that is current then, so that the first step
@@ -526,8 +528,10 @@ class AdamW:
         columns = [("m", self.m, size, kinds[0]), ("v", self.v, size, kinds[1])]
         if state_bits == 8:
             columns += [("m_scale", self.m_scale, per, torch.float32), ("v_scale", self.v_scale, per, torch.float32)]
+        self._held = []  # the moments' memory, which the table names, whatever becomes of the tensors given
         for column, ts, sizes, kind in columns:
             self._check(ts, sizes, kind, self._dev, column)
+            self._held += [t.detach() for t in ts]
             self._table[column] = [t.data_ptr() for t in ts]
         self._dtype = self.params[0].dtype
         self._watched = self.params + [t for t in self.copies if t is not None]
