@@ -764,3 +764,22 @@ def test_moments_stay_where_they_were_at_construction(bits):
         own.step(a["g"])
     torch.cuda.synchronize()
     assert torch.equal(p[0], a["p"][0]) and all((t == 7).all() for t in fresh)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e25, 2e30, 1e38, 3e38])
+def test_an_eps_near_the_end_of_float32(eps, bits):
+    """The quotient m / (root + eps) where eps is all of the denominator and its reciprocal no normal number. Gradients of
+    1e12 keep the quotient itself a normal number, and the learning rate brings it back to the size of the parameters."""
+    st = make([3000], bits=bits, seed=15)
+    p = st["p"][0].cpu().numpy()
+    st["g"][0].mul_(1e15)
+    (m,), (v,) = start_moments(st, bits)
+    hp = dict(lr=eps * 1e-13, betas=(0.9, 0.999), eps=eps, weight_decay=0.0)
+    AdamW(st["p"], state_bits=bits, seed=1, step=9, state=(st["m"], st["v"], st["ms"], st["vs"]), **hp).step(st["g"])
+    g = np64(st["g"][0])
+    want, _, _ = oo.adamw(p.astype(np.float64), g, m.astype(np.float64), v.astype(np.float64), hp["lr"], 0.9, 0.999, eps, 0.0, 10)
+    A = np.abs(0.9 * m.astype(np.float64)) + np.abs(0.1 * g)
+    tol = 16 * U * A * hp["lr"] / (1 - 0.9 ** 10) / eps + 4 * U * (np.abs(p) + np.abs(want))
+    moved = np.abs(want - p).max()
+    assert moved > 1e-3 and (np.abs(np64(st["p"][0]) - want) <= tol).all()

@@ -87,6 +87,7 @@ struct AdamwCoefs {
   double max_norm;  // 0: no clip
   uint32_t step, tensor0;  // the random bits' counter takes the low word of the step number
   double t;                // the bias corrections the whole of it
+  uint32_t usual;          // bits of the magnitude that the usual case of the 8-bit step stays below
   // read on the device instead of the host's numbers, where given
   const long long* step_dev;
   const double* lr_dev;
@@ -383,7 +384,8 @@ SVLA_DEV void general8(const AdamwCoefs& c, const Place<TP, TG, uint8_t>& a, con
 }
 
 // The usual case of the 8-bit step has |m| and v below 2^100: v's product with 2^24 is finite, and the reciprocals of
-// the scales are normal numbers.
+// the scales are normal numbers. So is that of the denominator, with an eps below 2^100 (AdamwCoefs::usual: 0 with a
+// larger one).
 constexpr uint32_t USUAL_MAG = (127u + 100u) << 23;
 SVLA_DEV float sqrt_approx(float x) {
   float r;
@@ -452,7 +454,7 @@ SVLA_DEV void update32(const AdamwCoefs& c, const Place<TP, TG, float>& a) {
   store_all(a, p, in.m, in.v);
 }
 
-// The usual case in packed pairs: every v positive, v and |m| below 2^100.
+// The usual case in packed pairs: every v positive, v, |m| and eps below 2^100.
 // Else the block is done by general8.
 template <typename TP, typename TG>
 SVLA_DEV void update8(const AdamwCoefs& c, const Place<TP, TG, uint8_t>& a, uint32_t block, uint32_t step, uint32_t tensor,
@@ -490,7 +492,7 @@ SVLA_DEV void update8(const AdamwCoefs& c, const Place<TP, TG, uint8_t>& a, uint
   }
   const uint32_t mxb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
   const uint32_t vxb = __reduce_max_sync(0xffffffffu, __float_as_uint(vx));
-  if (!__all_sync(0xffffffffu, vmin > 0.f && mxb < USUAL_MAG && vxb < USUAL_MAG)) {
+  if (!__all_sync(0xffffffffu, vmin > 0.f && mxb < c.usual && vxb < c.usual)) {
     general8(c, a, r);
     return;
   }
@@ -860,6 +862,7 @@ svla_status adamw_checked(const svla_adamw_tensor* ts, int n, const svla_adamw_a
   c.max_norm = a->max_norm;
   c.step = (uint32_t)a->step;
   c.t = (double)a->step;
+  c.usual = c.eps < 0x1p100f ? USUAL_MAG : 0u;
   c.step_dev = reinterpret_cast<const long long*>(a->step_device);
   c.lr_dev = a->lr_device;
   c.lr = a->lr;
