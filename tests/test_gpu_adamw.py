@@ -783,3 +783,55 @@ def test_an_eps_near_the_end_of_float32(eps, bits):
     tol = 16 * U * A * hp["lr"] / (1 - 0.9 ** 10) / eps + 4 * U * (np.abs(p) + np.abs(want))
     moved = np.abs(want - p).max()
     assert moved > 1e-3 and (np.abs(np64(st["p"][0]) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("at", [(0,), (300,), (255, 256), (599,)])
+def test_the_neighbours_of_a_gradient_that_is_not_finite(at, bad, bits):
+    """Only the elements concerned are lost: the others of their 256 step as the oracle's do, to codes and scales that
+    leave the lost ones out, and every other 256 bit for bit as without them (with 32 bits every other element)."""
+    sizes, hp = [600, 300], (1e-3, 0.9, 0.999, 1e-8, 1e-2)
+    ref, st = (make(sizes, bits=bits, seed=6) for _ in range(2))
+    for i in at:
+        st["g"][0][i] = bad
+    M, V = start_moments(st, bits)
+    before = ([x.cpu().numpy() for x in st["p"]], [x.cpu().numpy() for x in st["g"]], M, V)
+    for s in (ref, st):
+        AdamW(s["p"], state_bits=bits, seed=1, state=(s["m"], s["v"], s["ms"], s["vs"])).step(s["g"])
+    if bits == 8:
+        with np.errstate(all="ignore"):
+            check_step(st, before, bits, hp, 1, [True, True], 1, 0.0)
+    lost = torch.zeros(sizes[0], dtype=torch.bool, device=DEV)
+    lost[list(at)] = True
+    assert torch.isnan(st["p"][0][lost]).all() and torch.isfinite(st["p"][0][~lost]).all()
+    apart = ~lost
+    for i in at if bits == 8 else ():
+        apart[i // 256 * 256:i // 256 * 256 + 256] = False
+    for i, keep in ((0, apart), (1, torch.ones(sizes[1], dtype=torch.bool, device=DEV))):
+        assert keep.any()
+        for k in ("p", "m", "v"):
+            x, y = (s[k][i].view(torch.uint8).view(sizes[i], -1)[keep] for s in (st, ref))
+            assert torch.equal(x, y), (i, k)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_the_first_tensor_in_lists_of_every_length(bits):
+    """Alone, in a list of one launch's short table, past it, and past the long one: the same bits."""
+    outs = []
+    for count in (1, 32, 33, 400, 401, 900):
+        st = make([5000], bits=bits, seed=2)
+        more = [make([k], bits=bits, seed=20) for k in (300, 1, 0, 2049)]
+        lists = {k: None if st[k] is None else list(st[k]) for k in ("p", "g", "m", "v", "ms", "vs")}
+        for i in range(1, count):
+            for k in lists:
+                if lists[k] is not None:
+                    t = more[i % 4][k][0]
+                    lists[k].append(t if k == "g" else t.clone())
+        opt = AdamW(lists["p"], state_bits=bits, seed=4, state=(lists["m"], lists["v"], lists["ms"], lists["vs"]))
+        for _ in range(3):
+            opt.step(lists["g"])
+        outs.append(st)
+    for st in outs[1:]:
+        for k in ("p", "m", "v") + (("ms", "vs") if bits == 8 else ()):
+            assert torch.equal(outs[0][k][0].view(torch.uint8), st[k][0].view(torch.uint8)), k

@@ -432,3 +432,27 @@ def test_two_threads_with_two_widths_of_one_kernel(widths):
         want = make(9, D, x="bf16", y="bf16", seed=1)
         op_layernorm_backward(a["dy"], a["x"], a["gamma"], a["mean"], a["rstd"], want["dx"], want["dgamma"], want["dbeta"])
         assert all(torch.equal(a[k], want[k]) for k in ("dx", "dgamma", "dbeta"))
+
+
+def rows_a_block(D):
+    """Rows of a block of the backward's kernel: 256 threads of as many as a row's columns take."""
+    units = (D + 7) // 8
+    if units <= 16:
+        T = 1 << (units - 1).bit_length()
+    elif D <= 768:
+        T = 32
+    else:
+        nu = 2 if D <= 8192 else 3
+        T = min(512, 32 * -(-units // (32 * nu)))
+    return max(1, 256 // T)
+
+
+@pytest.mark.parametrize("D", [8, 96, 769, 771, 1024, 1025, 1536, 2048, 2056, 4096, 8200])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_blocks_of_the_backward_at_every_width(D, x):
+    """The full cluster of 8 blocks and the first count past it, rows of several warps and several such rows a block."""
+    R = rows_a_block(D)
+    need = [int(_abi.load().svla_op_layernorm_backward_workspace_bytes(m, D)) for m in (8 * R, 8 * R + 1)]
+    assert need[0] == 0 and need[1] > 0
+    for M in sorted({7 * R + 1, 8 * R - 1, 8 * R, 8 * R + 1, 16 * R + 1}):
+        check(M, D, x=x, y="bf16", seed=M)
