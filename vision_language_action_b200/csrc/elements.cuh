@@ -1,25 +1,12 @@
-// Loads and stores of 8 consecutive elements (16-byte accesses) or of one, fp32
-// or bf16 in memory and fp32 in registers (stores round to nearest even).
+// Loads of one element and stores of one or of 8 consecutive ones (16-byte
+// accesses), fp32 or bf16 in memory and fp32 in registers (stores round to
+// nearest even).
 #pragma once
 
 #include "common.cuh"
 
 namespace svla {
 
-SVLA_DEV void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-SVLA_DEV void load8(const uint16_t* p, float (&x)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    x[2 * k] = __uint_as_float(w[k] << 16);
-    x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-  }
-}
 SVLA_DEV float load1(const float* p) { return *p; }
 SVLA_DEV float load1(const uint16_t* p) { return bf2f(*p); }
 SVLA_DEV void store8(float* p, const float (&x)[8]) {

@@ -36,7 +36,6 @@
 #include <vector>
 
 #include "common.cuh"
-#include "elements.cuh"
 #include "pairs.cuh"
 #include "philox.cuh"
 
@@ -588,7 +587,7 @@ __global__ void __launch_bounds__(ADAMW_THREADS, BITS == 8 && sizeof(TP) == 2 ? 
       for (int w = 0; w < ADAMW_WARPS; ++w) all += part[w];
       const double norm = sqrt(all);
       if (blockIdx.x == 0 && grad_norm) *grad_norm = (float)norm;
-      // a norm that is not finite: 0 marks the step as skipped
+      // a norm that is not finite: -1 marks the step as skipped
       s_clip = norm <= 1.7976931348623157e308 ? (float)fmin(1.0, c.max_norm / (norm + 1e-6)) : -1.f;
     }
     __syncthreads();
