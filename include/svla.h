@@ -150,8 +150,8 @@ SVLA_API int svla_expert_weights(const svla_handle* h);
  * and the action and time projections train, the language model is frozen).
  * Readings: x_t = t_b eps + (1 - t_b) a per query, v = v(x_t, t_b | prefix),
  * loss = mean over the B H A terms of (v - (eps - a))^2; the result is the loss
- * and its gradient with respect to every expert and head tensor (no optimiser
- * update).
+ * and its gradient with respect to every expert and head tensor (the update is
+ * svla_train_update's).
  *   kv_cache, pad_mask: the frozen prefix, as for svla_denoise (device).
  *   actions: the target chunk a, noise: eps, device float32 [B, H, A];
  *   t: device float32 [B], the flow time of each query.
@@ -159,7 +159,8 @@ SVLA_API int svla_expert_weights(const svla_handle* h);
  *   grads: device float32, svla_train_grad_elems(h) elements, 16-byte aligned:
  *     every tensor of the blob from the first expert layer's in_norm to b_out,
  *     in manifest order and shape ([out, in] for matrices) (written in full).
- * The forward uses the weights given to svla_create_ex; work is stream-ordered
+ * The forward uses the weights given to svla_create_ex or, after a
+ * svla_train_update, those of the last one; work is stream-ordered
  * and bitwise reproducible (fixed-order reductions). The step runs as one CUDA
  * graph, captured on the first call with a given (B, L, H, buffers) and
  * replayed afterwards (like svla_denoise), so make that first call before
@@ -439,7 +440,9 @@ SVLA_API svla_status svla_op_rmsnorm(const float* x, const void* g, int M, int D
 
 /* LayerNorm, the norm of the vision side's layers (SigLIP, upstream of
  * svla_assemble_prefix: "noeira docs, SmolVLA" §Architecture), beside
- * svla_op_rmsnorm, with the backward pass that training them needs.
+ * svla_op_rmsnorm, with its backward pass. (The library computes no vision
+ * tower and svla_train_step trains the expert alone: these serve a caller's own
+ * layers.)
  *   forward, per row of D:  mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps),
  *     y = (x - mu) r gamma + beta
  *   backward, xh = (x - mu) r, w = dy gamma:
@@ -492,15 +495,18 @@ SVLA_API size_t svla_op_layernorm_backward_workspace_bytes(int M, int D);
  *   v_scale a float32 for every 256 consecutive elements of the tensor
  *   (ceil(n / 256)): moment = code * scale. The scale is the power of two that
  *   puts the largest magnitude of its 256 into [2^7, 2^8) (m) or [2^14, 2^15)
- *   (v); 0 where all are 0. Magnitudes are rounded up with the probability of
+ *   (v), 2^-120 (m) or 2^-112 (v) at least; 0 where all are 0. Magnitudes are rounded up with the probability of
  *   their distance to the lower code, from 16 random bits: Philox4x32-10 with
  *   key = seed, counter {k / 8 low, k / 8 high, t low, tensor index} for element k,
  *   half k % 8 of the 128 bits (low half of a word first). No subnormal codes:
- *   an m then below 2^-6 of its scale becomes 0, a v > 0 is at least 2^-14 of it.
+ *   an m then below 2^-6 of its scale becomes 0, a v > 0 is at least 2^-14 of it:
+ *   an element whose m is less than about 2^-13 of its block's largest keeps no
+ *   momentum, and rounding is right in the mean only above that.
  *   A moment that is not finite has the NaN code. Zero bytes are a valid start
  *   (all moments 0).
  * Pointers are of the current device. The table is read during the call only;
- * tensors of n = 0 are skipped. Pointers need their element type's alignment;
+ * tensors of n = 0 are skipped. One call has one param_type and one grad_type (a
+ * model of several takes a call for each, and each call's G is its own). Pointers need their element type's alignment;
  * tensors whose pointers are all aligned to 8 elements (32 bytes for float32,
  * 16 for bf16, 8 for codes) are read in wide accesses. Memory that is written may not overlap any other range of
  * the call (SVLA_ERR_ARG), so no tensor may be listed twice; gradients may be

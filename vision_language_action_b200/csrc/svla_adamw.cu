@@ -15,12 +15,17 @@
 // consecutive ones a lane.
 //
 // Measured (a step of 153 tensors, 99.8 M fp32 values with a bf16 copy): 32-bit
-// moments 461 us (6.5 TB/s, the rate of a copy), 540 with the clip, whose pass
+// moments 463 us (6.5 TB/s, the rate of a copy), 540 with the clip, whose pass
 // over the gradients is 61 us of reading; 8-bit moments 300 and 378 us (6.0
-// TB/s without the clip). 144 tensors, 157 M bf16 values, 8-bit moments: 381 us,
-// 4.2 TB/s: there the instructions bound it, 55 an element where the memory's
-// time is that of about 35 (decoding, the random bits and encoding; the
-// schedulers issue in 63 % of the cycles).
+// TB/s without the clip). 144 tensors, 157 M bf16 values, 8-bit moments: 384 us,
+// 4.1 TB/s, and neither limit is reached: memory alone would take 241 us, the
+// 268.5 M warp instructions (55 a value) 231 us of the schedulers (1965 MHz).
+// A warp loads, computes and stores its values in turn, and the 29 warps an SM
+// overlap the two too little (DRAM 48 %, issue 63 %); the 64 registers that let
+// four blocks on an SM also spill 32 bytes a thread.
+// Values whose second moment is 0 cost more (general8): with no gradient
+// anywhere 100 M fp32 values take 632 us (273 without such blocks, 440 with a
+// third of them), bf16 589 (239, 373).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -46,7 +51,10 @@ namespace {
 
 constexpr int ADAMW_BLOCK = 256;   // elements of a warp's task = elements that share a scale
 constexpr int ADAMW_CAP = 400;     // tensors of one launch (28.1 KB of the 32,764 bytes of kernel parameters)
-constexpr int ADAMW_FEW = 32;      // of a launch of a short list: the parameters are copied at every launch
+// Tensors of a launch of a short list: the parameters are copied at every launch (with the clip, 27 tensors 21.2 us a call
+// and 32 tensors 23.4; with the long table 23.4 and 25.3. A longer short table would serve more lists: one of 128 took 33
+// tensors in 22.4 us a call, the long one 26.6).
+constexpr int ADAMW_FEW = 32;
 constexpr int ADAMW_HINTS = 256;   // spans of chunks whose first tensor the table names
 constexpr int ADAMW_THREADS = 256;
 constexpr int ADAMW_WARPS = ADAMW_THREADS / 32;
@@ -246,13 +254,16 @@ SVLA_DEV void pack(const float (&x)[8], Raw8<uint16_t>& r) {
 // Codes of the 8-bit moments: the top bits of the fp32 magnitude, its exponent
 // counted from a power of two that the block's largest finite magnitude sets.
 // u20 (16 random bits << 4) enters at the top of the dropped bits: the code is
-// rounded up with the probability of its distance to the lower code, so the
-// stored moment is right in the mean. Nearest rounding would hold v where it
-// is: a step moves v by (1 - b2) ~ 1e-3 of itself and the codes lie 1/8 to 1/4
-// apart.
+// rounded up with the probability of its distance to the lower code, so a
+// stored moment of the codes' range is right in the mean. Nearest rounding would
+// hold v where it is: a step moves v by (1 - b2) ~ 1e-3 of itself and the codes
+// lie 1/8 to 1/4 apart.
 //   m: e4m3, largest magnitude in [2^7, 2^8) of the scale; below 2^-6 -> 0
 //   v: e5m2, largest in [2^14, 2^15); 0 < v below 2^-14 -> 2^-14, so no
 //      gradient is ever divided by a vanished v
+// Below the range there is a bias: an m of less than 2^-13 or so of its block's
+// largest keeps no momentum (its step is that of 1 - b1 of the gradient while
+// that lasts), a v of less than 2^-28 or so of it is too large.
 // Subnormal codes are not made. Values that are not finite are put in later.
 SVLA_DEV uint32_t encode_m(float x, uint32_t u20, uint32_t low) {
   const uint32_t bits = __float_as_uint(x);
@@ -462,7 +473,8 @@ SVLA_DEV void update8(const AdamwCoefs& c, const Place<TP, TG, uint8_t>& a, uint
   in.load(a);
   const float ms = *a.ms, vs = *a.vs;
   // 16 random bits of element k: half k % 8 of the draw of its octet k / 8; both moments take the same bits
-  // (each is right in the mean by itself, and the ratio's error is smaller when they round the same way)
+  // (each is right in the mean by itself in the codes' range, and the ratio's error is smaller when they round the same
+  // way)
   const unsigned long long oct = (unsigned long long)block * 32 + lane;
   uint32_t r[4] = {(uint32_t)oct, (uint32_t)(oct >> 32), step, tensor};
 #pragma unroll

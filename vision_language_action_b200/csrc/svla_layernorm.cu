@@ -15,8 +15,9 @@
 //
 // Both are bound by memory where there are many rows, by latency where there are
 // few. Measured: forward of 65536 x 768, fp32 in and bf16 out, 51.5 us (5.9
-// TB/s); backward of 16384 rows, bf16: 768 wide 22 us (3.4 TB/s), 4096 wide 81
-// us (5.0 TB/s). One row 2.9 us, 50 rows backward 5.8 us: a launch.
+// TB/s); backward of 16384 rows, bf16: 768 wide 22 us (3.4 TB/s), 4096 wide 82
+// us (4.9 TB/s); of 4000 rows 12288 wide 75 us (3.9 TB/s), 16384 wide 117 us (3.4
+// TB/s). One row 3.1 us, 50 rows backward 6.1 us: a launch.
 #include <algorithm>
 #include <atomic>
 #include <exception>
@@ -77,7 +78,8 @@ LnPlan ln_fwd_plan(int D, bool vec, bool bf16_x) {
 // Backward: 16 sums and, per unit, 4 (bf16) or 8 (fp32) registers of x and of dy have to fit beside the rest in the 128
 // registers of 512 threads an SM. One warp a row up to 768 columns (three units a thread); then two units while 512
 // threads hold the row so (the next row's registers fit beside it: 16384 bf16 rows of 4096 in 81 us; three units 94),
-// then three. What is wider than 12288 keeps its columns' sums in shared memory.
+// then three (which do not quite fit: 36 to 144 bytes of spills a thread with the wide accesses, 120 to 248 without). What
+// is wider than 12288 keeps its columns' sums in shared memory.
 LnPlan ln_bwd_plan(int D) { return D <= 768 ? ln_plan(D, 3, 32) : ln_plan(D, D <= 8192 ? 2 : 3, 512); }
 
 int ln_bwd_blocks(int M, const LnPlan& p, int per_sm) {
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(STEP == STEP_T ? 256 : 512)
       prefetch_row(dyp + (row + stride) * a.lddy, D, T, tid);
     }
     f32x2 w2 = both(0.f), x2 = both(0.f);  // sums of w and of w xh
-    f32x2 xhs[NU * 4], ws[NU * 4];         // kept for dx (4000 bf16 rows of 12288: 75 us, 82 computed twice)
+    f32x2 xhs[NU * 4], ws[NU * 4];         // kept for dx (4000 bf16 rows of 12288: 75 us, 82 computed twice, which spills less)
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       if (!KEEP) g.load(reinterpret_cast<const TW*>(a.gamma), D, T, tid, u);

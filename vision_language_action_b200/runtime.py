@@ -475,8 +475,8 @@ class AdamW:
     tensors (the scales None with 32 bits), resumes with those moments and ``step`` with that many steps taken. The
     moments stay where they are at construction: load others with ``copy_`` into ``m``, ``v`` and their scales
     (parameters and copies are followed to storage that they are given).
-    ``capturable`` counts the steps on the device, so that a captured ``step`` counts on at every replay; ``lr``
-    may then be a float64 CUDA tensor of one element, read at every step. A step without it that is captured repeats
+    ``capturable`` counts the steps on the device, in ``step_tensor``, so that a captured ``step`` counts on at every
+    replay (``steps`` counts calls: resume with ``step=int(step_tensor)``); ``lr`` may then be a float64 CUDA tensor of one element, read at every step. A step without it that is captured repeats
     its own step number at every replay. The constructor waits for the stream that is current then, so that the first step
     may run on any other (the tensors given are the caller's to order, and so are steps on different streams).
     Autograd does not see the parameters change: step between a backward pass and
